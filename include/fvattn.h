@@ -69,7 +69,8 @@ typedef enum {
     FVATTN_ERR_CAPACITY = -4,       /* workspace or col_idx capacity too small */
     FVATTN_ERR_CUDA = -5,           /* a CUDA runtime/driver call failed */
     FVATTN_ERR_BAD_CSR = -6,        /* device: index out of range, not ascending, count > nb */
-    FVATTN_ERR_DEVICE_TIMEOUT = -7  /* device: a bounded wait gave up */
+    FVATTN_ERR_DEVICE_TIMEOUT = -7, /* device: a bounded wait gave up */
+    FVATTN_ERR_BAD_PAGE = -8        /* device: a page table entry, length or count out of range */
 } fvattn_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -442,6 +443,120 @@ FVATTN_API int64_t fvattn_attn_num_items(int B, int H, int N, int block);
 FVATTN_API int fvattn_attn_work_order(const int32_t *row_ptr, const int32_t *col_idx, int B, int H, int N, int block,
                                       int32_t *order, void *workspace, size_t ws_bytes, int32_t *dev_status,
                                       fvattn_stream_t stream);
+
+/*
+ * fvattn_rope -- rotary positions with several axes, the step between the
+ * projections and fvattn_route / fvattn_sparse_fwd: the tokens of a video stand on a
+ * (time, height, width) grid, and each coordinate turns its own share of a head's
+ * channel pairs.
+ *   theta(t, j) = pos[t, pair_axis[j]] * inv_freq[j]                 j = 0 .. n_pairs - 1
+ *   y_a = x_a cos theta - x_b sin theta,  y_b = x_b cos theta + x_a sin theta
+ * with (a, b) = (2j, 2j + 1) for pairing 0 ("interleaved") and (j, j + n_pairs) for pairing 1
+ * ("half").  Channels from 2 n_pairs on pass through, bit for bit.  inverse = 1 turns by
+ * -theta: the transpose of the rotation, so it takes the gradients dQ, dK of
+ * fvattn_sparse_bwd to those of the unrotated Q and K.
+ *   Q, Qr         device bf16 [B, q_heads, N, d], in and out, element (b, h, t, c) at
+ *                 b * s[0] + h * s[1] + t * s[2] + c with the host arrays q_strides and
+ *                 qr_strides (in elements, multiples of 8, not negative): a projection's
+ *                 [B, N, H, d] or a fused [B, N, 3, H, d] is read in place.  Qr may be Q
+ *                 with the same strides (in place); any other overlap is undefined.  The
+ *                 rows of Qr must not overlap each other.
+ *   K, Kr         the same with k_heads; both null with k_heads 0 to turn one tensor.
+ *   pos           device int32 [N, n_axes], or [B, N, n_axes] with pos_batch_stride =
+ *                 N * n_axes (0: one for all sequences).  Any int32 value; angles are reduced
+ *                 in fp64.
+ *   inv_freq      host double[n_pairs], finite.   pair_axis  host int32[n_pairs] in [0, n_axes).
+ *                 Both are read during the call only.
+ * 1 <= n_axes <= 4; 1 <= n_pairs <= d/2, a multiple of 8 for pairing 1; d in {64, 128}; N >= 1;
+ * B <= 65535.  Products in fp32, one rounding to bf16.  Asynchronous on `stream`; no workspace
+ * and no device errors.
+ */
+FVATTN_API int fvattn_rope(const void *Q, const int64_t *q_strides, void *Qr, const int64_t *qr_strides, int q_heads,
+                           const void *K, const int64_t *k_strides, void *Kr, const int64_t *kr_strides, int k_heads,
+                           int B, int N, int d, const int32_t *pos, int64_t pos_batch_stride, const double *inv_freq,
+                           const int32_t *pair_axis, int n_pairs, int n_axes, int pairing, int inverse,
+                           fvattn_stream_t stream);
+
+/*
+ * The paged 8-bit cache of keys and values (fvattn_cache_append, fvattn_cache_attend).
+ *
+ *   k_codes, v_codes  device uint8 [num_pages, heads, block, d], 16-byte aligned: e4m3 codes in
+ *                     the format of fvattn_quant_e4m3.
+ *   k_exp, v_exp      device int32 [num_pages, heads]: a code's value is its e4m3 value times
+ *                     2^exponent (one scale per block of tokens and head).
+ *   page_table        device int32 [B, max_pages]: page i of sequence b holds its tokens
+ *                     i * block .. i * block + block - 1, in their order.
+ * block in {64, 128}, d in {64, 128}, max_pages * block < 2^30.  The caller owns the pool, hands
+ * out pages and keeps the lengths.  A page may stand in several sequences' tables as long
+ * as no call appends to it (appending to a page that two sequences share is undefined: copy it
+ * first).  Nothing is read or written in pages that a call's lengths do not reach.
+ */
+
+/*
+ * fvattn_cache_append -- new keys and values behind the cached ones, the keys turned by
+ * their rotary positions on the way (as fvattn_rope, without the rounding to bf16).
+ *   K, V          device bf16 [B, heads, T, d], strides as fvattn_rope's inputs.
+ *   start         device int32 [B]: cached tokens of each sequence before the call; token t of
+ *                 sequence b goes to place start[b] + t.
+ *   new_lens      device int32 [B], 0 .. T valid tokens of each sequence, or null: T for all.
+ *                 The rows behind them are not read.
+ *   pos           device int32 [T, n_axes] or [B, T, n_axes] (pos_batch_stride as fvattn_rope),
+ *                 with inv_freq, pair_axis, n_pairs, n_axes and pairing; or null: no rotation.
+ * Per touched (page, head), for K and for V: with a the largest magnitude among the page's new
+ * values and need the smallest e with a 2^-e <= 448 (0 if one is infinite), the exponent becomes
+ * max(old, need) where the page holds earlier tokens of the sequence and need where it does
+ * not.  New values are rounded once, from fp32, to the nearest e4m3 value (ties to even,
+ * saturating at 448, NaN kept).  Where the exponent grew, the earlier tokens' codes are
+ * moved to it (exact except where they become subnormal; those are rounded to nearest).  A page
+ * whose tokens are all zero gets the exponent -160, which any later value replaces.  Places
+ * behind the new tokens are left as they were.  Appending the same tokens at the same place
+ * again gives the same page.
+ * *dev_status (written by the call): FVATTN_ERR_BAD_PAGE where start < 0, new_lens outside [0, T],
+ * start + new > max_pages * block, or a touched page table entry outside [0, num_pages); the
+ * tokens concerned are left out, the others are appended.  One launch, no workspace.
+ */
+FVATTN_API int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, const int64_t *v_strides,
+                                   int B, int heads, int T, int d, int block, uint8_t *k_codes, int32_t *k_exp,
+                                   uint8_t *v_codes, int32_t *v_exp, int num_pages, const int32_t *page_table,
+                                   int max_pages, const int32_t *start, const int32_t *new_lens, const int32_t *pos,
+                                   int64_t pos_batch_stride, const double *inv_freq, const int32_t *pair_axis,
+                                   int n_pairs, int n_axes, int pairing, int32_t *dev_status, fvattn_stream_t stream);
+
+/* Device workspace fvattn_cache_attend needs, in bytes (0 on bad arguments).  Up to 32 rows
+ * (group * M) it holds the partial results of the split; above, the pages as bf16
+ * (B * heads * max_pages * block * d * 4 bytes). */
+FVATTN_API size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block,
+                                                      int max_pages);
+
+/*
+ * fvattn_cache_attend -- exact attention of each sequence's M newest tokens over its
+ * cached keys and values (FlashAttention review §Model: one pass, running maximum and sum).
+ *   Q, O          device bf16 [B, heads * group, M, d], strides as fvattn_rope's (O's rows must
+ *                 not overlap); query head h reads key head h / group.
+ *   lens          device int32 [B]: cached tokens, the new ones among them (after the append).
+ *   new_lens      device int32 [B], 0 .. M query tokens of each sequence, or null: M for all.
+ *                 Rows behind them are neither read nor written in O and LSE.
+ *   causal        1: query token m sees cached tokens u <= lens - new_lens + m; 0: all lens.
+ *   LSE           out, fp32 [B, heads * group, M], natural logarithm.
+ * A query that sees no token (an empty sequence) gets O = 0 and LSE = -inf.  What a query does
+ * not see, NaN codes and places behind the sequence's end among it, does not reach its row.
+ * Up to 32 rows (group * M): the weights are rounded to fp16 before P V and the cached tokens
+ * are split over the SMs and joined in a fixed order.  Above: the pages are expanded to bf16
+ * (exact) in the workspace and the tensor cores' 128-row tiles run over them, with P rounded to
+ * bf16 as in fvattn_sparse_fwd.  Both sum in fp32.  The result does not depend on what else
+ * runs; no atomics on floating values.
+ * *dev_status (written by the call): FVATTN_ERR_BAD_PAGE where lens is outside [0, max_pages *
+ * block], new_lens outside [0, M] (both are clamped), or an entry of the page table in use is
+ * outside [0, num_pages) (above 32 rows its tokens count as zeros, up to 32 rows they are left out:
+ * the result is not to be used); FVATTN_ERR_DEVICE_TIMEOUT as fvattn_sparse_fwd.
+ * B <= 4096; B * heads * max_pages * block / 64 < 2^31; group * M < 2^24.
+ */
+FVATTN_API int fvattn_cache_attend(const void *Q, const int64_t *q_strides, int B, int heads, int group, int M, int d,
+                                   int block, const uint8_t *k_codes, const int32_t *k_exp, const uint8_t *v_codes,
+                                   const int32_t *v_exp, int num_pages, const int32_t *page_table, int max_pages,
+                                   const int32_t *lens, const int32_t *new_lens, int causal, void *O,
+                                   const int64_t *o_strides, float *LSE, void *workspace, size_t ws_bytes,
+                                   int32_t *dev_status, fvattn_stream_t stream);
 
 /* Compiled-in build description (architecture, version), static string. */
 FVATTN_API const char *fvattn_build_info(void);

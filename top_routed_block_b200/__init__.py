@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple, Sequence
 
 import torch
 
@@ -34,6 +35,7 @@ FVATTN_ERR_CAPACITY = -4
 FVATTN_ERR_CUDA = -5
 FVATTN_ERR_BAD_CSR = -6
 FVATTN_ERR_DEVICE_TIMEOUT = -7
+FVATTN_ERR_BAD_PAGE = -8
 
 _lib = None
 
@@ -85,6 +87,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "fvattn_sparse_fwd_fp8": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, SZ, P, P]),
         "fvattn_bwd_workspace_bytes": (SZ, [I, I, I, I]),
         "fvattn_sparse_bwd": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, SZ, P, P]),
+        "fvattn_rope": (I, [P, P, P, P, I, P, P, P, P, I, I, I, I, P, I64, P, P, I, I, I, I, P]),
+        "fvattn_cache_append": (I, [P, P, P, P, I, I, I, I, I, P, P, P, P, I, P, I, P, P, P, I64, P, P, I, I, I, P,
+                                    P]),
+        "fvattn_cache_attend_workspace_bytes": (SZ, [I, I, I, I, I, I, I]),
+        "fvattn_cache_attend": (I, [P, P, I, I, I, I, I, I, P, P, P, P, I, P, I, P, P, I, P, P, P, P, SZ, P, P]),
         "fvattn_attention_host": (I, [P, P, P, I, I, I, I, I, D, I, P, P, P, P, P, P, P, P, P, I64, P, P, SZ, P, SZ,
                                       P, P]),
     }
@@ -426,6 +433,251 @@ def fvattn_sparse_fwd_noalloc(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
     return O, LSE, dev_status
 
 
+# ------------------------------------------------------- rotary positions, 8-bit cache
+
+PAIRINGS = {"interleaved": 0, "half": 1}
+
+
+class RopeAxes(NamedTuple):
+    """What turns a head's channel pairs: per pair an angle per unit of position and the
+    axis (column of the positions) it goes by; ``pairing`` says which two channels
+    make pair j: (2j, 2j + 1) "interleaved" or (j, j + pairs) "half"."""
+    inv_freq: Sequence[float]
+    pair_axis: Sequence[int]
+    pairing: str = "interleaved"
+
+
+def rope_axes(dims: Sequence[int], theta: float = 10000.0, pairing: str = "interleaved") -> RopeAxes:
+    """Frequencies theta^(-2j/n) over n channels for each axis of ``dims`` in turn: e.g.
+    (44, 42, 42) channels of d = 128 by time, height and width."""
+    import numpy as np
+    if any(n < 0 or n % 2 for n in dims):
+        raise ValueError("each axis takes an even number of channels")
+    freq = [theta ** (-2.0 * j / n) for n in dims for j in range(n // 2)]
+    axis = [i for i, n in enumerate(dims) for _ in range(n // 2)]
+    return RopeAxes(np.array(freq, dtype=np.float64), np.array(axis, dtype=np.int32), pairing)
+
+
+def grid_positions(T: int, H: int, W: int, *, first_frame: int = 0, device="cuda") -> torch.Tensor:
+    """Positions int32 [T*H*W, 3] (time, height, width) of a video's tokens, time slowest."""
+    t = torch.arange(first_frame, first_frame + T, dtype=torch.int32, device=device)
+    y, x = (torch.arange(n, dtype=torch.int32, device=device) for n in (H, W))
+    return torch.stack(torch.meshgrid(t, y, x, indexing="ij"), -1).reshape(-1, 3).contiguous()
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _heads_tensor(t: torch.Tensor, what: str):
+    """(B, H, n, d) and the strides of a bf16 CUDA tensor whose channels are contiguous."""
+    if t.dim() != 4 or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA bf16 tensor [B, H, n, d]")
+    shape, st = t.shape, t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{what}: the channels of a head must be contiguous")
+    return tuple(shape), _Strides(*(0 if n == 1 else x for n, x in zip(shape[:3], st)))
+
+
+def _int32(t: torch.Tensor | None, shape, what: str, device) -> None:
+    if t is None:
+        return
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what}: expected a contiguous int32 tensor {list(shape)} on {device}")
+
+
+def _status_word(t: torch.Tensor, device) -> None:
+    if t.dtype != torch.int32 or t.numel() < 1 or t.device != device:
+        raise ValueError(f"dev_status: expected an int32 tensor on {device}")
+
+
+class _On:
+    """A call on ``device``: makes it current if it is not, and gives the stream (the
+    caller's, or the device's current one).  Tensors made inside for a stream that is
+    not current are kept from reuse until that stream has passed them."""
+
+    def __init__(self, device: torch.device, stream):
+        self.switch = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self.device, self.other = device, stream
+
+    def __enter__(self):
+        if self.switch is not None:
+            self.switch.__enter__()
+        self.stream = int((self.other or torch.cuda.current_stream(self.device)).cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self.switch is not None:
+            self.switch.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+
+def _rope_args(rope: RopeAxes, positions: torch.Tensor, B: int, n: int, device):
+    """(arrays kept alive, C arguments from the positions to the pairing)."""
+    import numpy as np
+    freq = np.ascontiguousarray(rope.inv_freq, dtype=np.float64)
+    axis = np.ascontiguousarray(rope.pair_axis, dtype=np.int32)
+    if freq.ndim != 1 or axis.shape != freq.shape:
+        raise ValueError("rope: inv_freq and pair_axis are two lists of the same length")
+    if rope.pairing not in PAIRINGS:
+        raise ValueError(f"rope: pairing is one of {sorted(PAIRINGS)}")
+    if positions.dim() not in (2, 3):
+        raise ValueError("positions: expected [n, axes] or [B, n, axes]")
+    axes = positions.shape[-1]
+    _int32(positions, (n, axes) if positions.dim() == 2 else (B, n, axes), "positions", device)
+    return (freq, axis), (positions.data_ptr(), 0 if positions.dim() == 2 else n * axes, freq.ctypes.data,
+                          axis.ctypes.data, freq.size, axes, PAIRINGS[rope.pairing])
+
+
+def fvattn_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, rope: RopeAxes, *,
+                inverse: bool = False, out_q: torch.Tensor | None = None, out_k: torch.Tensor | None = None,
+                stream=None):
+    """Rotary positions with several axes on Q and K (bf16 [B, H, N, d], any strides with
+    contiguous channels, e.g. ``x.view(B, N, H, d).transpose(1, 2)`` of a projection; K may
+    be None).  positions: int32 [N, axes] or [B, N, axes].  Returns the turned Q and K,
+    contiguous unless out_q / out_k are given (which may be Q and K themselves)."""
+    lib = load_library()
+    (B, H, N, d), qs = _heads_tensor(Q, "Q")
+    dev = Q.device
+    if K is None and out_k is not None:
+        raise ValueError("out_k without K")
+    with _On(dev, stream) as on:
+        keep, args = _rope_args(rope, positions, B, N, dev)
+        outs, ptrs = [], []
+        for x, out, what in ((Q, out_q, "Q"), (K, out_k, "K")):
+            if x is None:
+                outs.append(None)
+                ptrs += [None, None, None, None, 0]
+                continue
+            shape, st = (Q.shape, qs) if x is Q else _heads_tensor(x, what)
+            if (shape[0], shape[2], shape[3]) != (B, N, d) or x.device != dev:
+                raise ValueError("K must match Q in all but its heads")
+            if out is None:
+                out = on.empty(tuple(shape), torch.bfloat16)
+            oshape, ost = _heads_tensor(out, f"out of {what}")
+            if tuple(oshape) != tuple(shape) or out.device != dev:
+                raise ValueError(f"out of {what}: wrong shape or device")
+            outs.append(out)
+            ptrs += [x.data_ptr(), st, out.data_ptr(), ost, shape[1]]
+        rc = lib.fvattn_rope(*ptrs, B, N, d, *args, 1 if inverse else 0, on.stream)
+    _check(rc, "fvattn_rope")
+    return outs[0], outs[1]
+
+
+def fvattn_rope_bwd(dQ: torch.Tensor, dK: torch.Tensor | None, positions: torch.Tensor, rope: RopeAxes, *,
+                    out_q: torch.Tensor | None = None, out_k: torch.Tensor | None = None, stream=None):
+    """Gradients of the unturned Q and K from those of the turned ones: the inverse rotation
+    (out_q / out_k: where they go, e.g. views of the projections' gradient)."""
+    return fvattn_rope(dQ, dK, positions, rope, inverse=True, out_q=out_q, out_k=out_k, stream=stream)
+
+
+class KvPages(NamedTuple):
+    """A pool of pages: e4m3 codes uint8 [pages, heads, block, d] and scale exponents int32
+    [pages, heads], for keys and for values."""
+    k_codes: torch.Tensor
+    k_exp: torch.Tensor
+    v_codes: torch.Tensor
+    v_exp: torch.Tensor
+
+
+def _pool_args(pages: KvPages, page_table: torch.Tensor, B: int, heads: int, d: int, device):
+    """Checks; returns (block, C arguments from the codes to max_pages)."""
+    k = pages.k_codes
+    if k.dim() != 4 or k.shape[1] != heads or k.shape[3] != d:
+        raise ValueError("pages: expected codes [pages, heads, block, d] matching K")
+    for t in (k, pages.v_codes):
+        if t.dtype != torch.uint8 or t.shape != k.shape or not t.is_contiguous() or t.device != device:
+            raise ValueError("pages: codes are contiguous uint8 tensors of one shape")
+    for t in (pages.k_exp, pages.v_exp):
+        _int32(t, k.shape[:2], "page exponents", device)
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected int32 [B, max_pages]")
+    _int32(page_table, (B, page_table.shape[1]), "page_table", device)
+    return int(k.shape[2]), (k.data_ptr(), pages.k_exp.data_ptr(), pages.v_codes.data_ptr(), pages.v_exp.data_ptr(),
+                             k.shape[0], page_table.data_ptr(), page_table.shape[1])
+
+
+def fvattn_cache_append(K: torch.Tensor, V: torch.Tensor, pages: KvPages, page_table: torch.Tensor,
+                        start: torch.Tensor, *, new_lens: torch.Tensor | None = None,
+                        positions: torch.Tensor | None = None, rope: RopeAxes | None = None,
+                        dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """New keys and values (bf16 [B, heads, T, d], strided as in fvattn_rope) behind the
+    start[b] cached tokens of each sequence, the keys turned by ``positions`` and ``rope`` if
+    given.  Returns dev_status (FVATTN_ERR_BAD_PAGE: read it after the stream)."""
+    lib = load_library()
+    (B, H, T, d), ks = _heads_tensor(K, "K")
+    vshape, vs = _heads_tensor(V, "V")
+    dev = K.device
+    if vshape != (B, H, T, d) or V.device != dev:
+        raise ValueError("K and V must have one shape")
+    if (positions is None) != (rope is None):
+        raise ValueError("positions and rope belong together")
+    block, pool = _pool_args(pages, page_table, B, H, d, dev)
+    _int32(start, (B,), "start", dev)
+    _int32(new_lens, (B,), "new_lens", dev)
+    with _On(dev, stream) as on:
+        keep, args = (None, (None, 0, None, None, 0, 0, 0)) if rope is None else _rope_args(rope, positions, B, T, dev)
+        if dev_status is None:
+            dev_status = on.empty((1,), torch.int32)
+        _status_word(dev_status, dev)
+        rc = lib.fvattn_cache_append(K.data_ptr(), ks, V.data_ptr(), vs, B, H, T, d, block, *pool, start.data_ptr(),
+                                     _ptr(new_lens), *args, dev_status.data_ptr(), on.stream)
+    _check(rc, "fvattn_cache_append")
+    return dev_status
+
+
+def fvattn_cache_attend_workspace_bytes(B: int, heads: int, group: int, M: int, d: int, block: int,
+                                        max_pages: int) -> int:
+    return int(load_library().fvattn_cache_attend_workspace_bytes(B, heads, group, M, d, block, max_pages))
+
+
+def fvattn_cache_attend(Q: torch.Tensor, pages: KvPages, page_table: torch.Tensor, lens: torch.Tensor, *,
+                        new_lens: torch.Tensor | None = None, causal: bool = False, O: torch.Tensor | None = None,
+                        LSE: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        dev_status: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's newest tokens (Q bf16 [B, heads * group, M, d], strided
+    as in fvattn_rope) over its lens[b] cached ones, the new ones among them.  Returns
+    (O bf16, LSE fp32, dev_status); rows behind new_lens[b] are left as they were."""
+    lib = load_library()
+    (B, Hq, M, d), qs = _heads_tensor(Q, "Q")
+    dev = Q.device
+    heads = int(pages.k_codes.shape[1]) if pages.k_codes.dim() == 4 else 0
+    if heads < 1 or Hq % heads:
+        raise ValueError("Q has a multiple of the cache's heads")
+    block, pool = _pool_args(pages, page_table, B, heads, d, dev)
+    _int32(lens, (B,), "lens", dev)
+    _int32(new_lens, (B,), "new_lens", dev)
+    group = Hq // heads
+    with _On(dev, stream) as on:
+        if O is None:
+            O = on.empty((B, Hq, M, d), torch.bfloat16)
+        oshape, ost = _heads_tensor(O, "O")
+        if LSE is None:
+            LSE = on.empty((B, Hq, M), torch.float32)
+        if oshape != (B, Hq, M, d) or O.device != dev:
+            raise ValueError("O must match Q")
+        if tuple(LSE.shape) != (B, Hq, M) or LSE.dtype != torch.float32 or not LSE.is_contiguous() or LSE.device != dev:
+            raise ValueError("LSE: expected contiguous fp32 [B, H, M]")
+        if dev_status is None:
+            dev_status = on.empty((1,), torch.int32)
+        _status_word(dev_status, dev)
+        if workspace is None:
+            need = lib.fvattn_cache_attend_workspace_bytes(B, heads, group, M, d, block, pool[-1])
+            workspace = on.empty((max(int(need), 16),), torch.uint8)
+        elif not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("workspace: expected a contiguous tensor on Q's device")
+        rc = lib.fvattn_cache_attend(Q.data_ptr(), qs, B, heads, group, M, d, block, *pool, lens.data_ptr(),
+                                     _ptr(new_lens), 1 if causal else 0, O.data_ptr(), ost, LSE.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                     dev_status.data_ptr(), on.stream)
+    _check(rc, "fvattn_cache_attend")
+    return O, LSE, dev_status
+
+
 def check_status(dev_status: torch.Tensor, where: str = "device") -> None:
     """Synchronise and raise if a kernel recorded an error."""
     torch.cuda.synchronize(dev_status.device)
@@ -451,6 +703,7 @@ class FvattnPlan:
         self.O = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
         self.LSE = torch.empty((B, H, N), dtype=torch.float32, device=dev)
         self.status = torch.zeros(3, dtype=torch.int32, device=dev)   # route, attention, first error (host path)
+        self.turned = None   # (Q, K) as attended, after a call with rotary positions
 
     def run_route(self, Q, K, p, stream=None) -> RouteResult:
         return fvattn_route(Q, K, p, self.block, stream=stream, out=self.route, workspace=self.route_ws)
@@ -461,13 +714,54 @@ class FvattnPlan:
         return fvattn_sparse_fwd(Q, K, V, rp, ci, self.block, causal, stream=stream, O=self.O, LSE=self.LSE,
                                  workspace=self.fwd_ws, dev_status=self.status[1:])
 
-    def __call__(self, Q, K, V, p, causal=False, stream=None):
+    def __call__(self, Q, K, V, p, causal=False, stream=None, positions=None, rope=None):
+        """Routing and attention; with ``positions`` and ``rope`` Q and K (any strides) are turned
+        first and stay in ``turned``, which is what fvattn_sparse_bwd takes."""
+        if (positions is None) != (rope is None):
+            raise ValueError("positions and rope belong together")
+        if rope is not None:
+            self.turned = Q, K = fvattn_rope(Q, K, positions, rope, stream=stream)
         self.run_route(Q, K, p, stream=stream)
         return self.run_fwd(Q, K, V, causal, stream=stream)
 
     def check(self):
         self.status[0:1].copy_(self.route.dev_status)
         check_status(self.status[:2], "fvattn")
+
+
+class FvattnCache:
+    """A paged e4m3 cache of one attention layer: a pool, each sequence's pages and lengths.
+
+    Pages are handed out in order, max_tokens / block to a sequence; a caller that shares
+    or recycles pages writes ``page_table`` itself (or calls the functions on its own pool:
+    layers of one model share the table and the lengths)."""
+
+    def __init__(self, B: int, heads: int, d: int, block: int, max_tokens: int, device="cuda"):
+        dev = torch.empty(0, device=device).device
+        per_seq = num_blocks(max_tokens, block)
+        shape = (B * per_seq, heads, block, d)
+        self.pages = KvPages(torch.zeros(shape, dtype=torch.uint8, device=dev),
+                             torch.zeros(shape[:2], dtype=torch.int32, device=dev),
+                             torch.zeros(shape, dtype=torch.uint8, device=dev),
+                             torch.zeros(shape[:2], dtype=torch.int32, device=dev))
+        self.page_table = torch.arange(B * per_seq, dtype=torch.int32, device=dev).view(B, per_seq)
+        self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(2, dtype=torch.int32, device=dev)   # append, attention
+
+    def append(self, K, V, *, new_lens=None, positions=None, rope=None):
+        """Appends K and V (bf16 [B, heads, T, d]) and moves the lengths on (current stream)."""
+        fvattn_cache_append(K, V, self.pages, self.page_table, self.lens, new_lens=new_lens, positions=positions,
+                            rope=rope, dev_status=self.status)
+        self.lens.add_(K.shape[2] if new_lens is None else new_lens)
+
+    def attend(self, Q, *, new_lens=None, causal=True, O=None, LSE=None):
+        """Attention of the tokens appended last over all cached ones; returns (O, LSE)."""
+        O, LSE, _ = fvattn_cache_attend(Q, self.pages, self.page_table, self.lens, new_lens=new_lens, causal=causal,
+                                        O=O, LSE=LSE, dev_status=self.status[1:])
+        return O, LSE
+
+    def check(self):
+        check_status(self.status, "fvattn cache")
 
 
 def fvattn_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Tensor, p: float, block: int,
@@ -485,5 +779,6 @@ def fvattn_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Tensor, 
     _check(rc, "fvattn_attention_host")
 
 
-__all__ = [n for n in dir() if n.startswith("fvattn_")] + ["FvattnPlan", "FvattnError", "RouteResult",
+__all__ = [n for n in dir() if n.startswith("fvattn_")] + ["FvattnPlan", "FvattnCache", "FvattnError", "RouteResult",
+                                                          "RopeAxes", "KvPages", "rope_axes", "grid_positions",
                                                           "check_status", "load_library", "status_string"]

@@ -1,6 +1,6 @@
 // abi.cu -- the extern "C" surface of libfvattn.so (declared in include/fvattn.h):
 // argument checks, workspace carving, TMA descriptor encoding and launches.
-// All compute runs in the kernels of route.cu, lpt.cu and attn_fwd.cu.
+// All compute runs in the kernels of the other files.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -13,9 +13,11 @@
 #include "fvattn.h"
 #include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
+#include "cache.cuh"
 #include "common.cuh"
 #include "lpt.cuh"
 #include "quant.cuh"
+#include "rope.cuh"
 #include "route.cuh"
 #include "sasa.cuh"
 
@@ -180,6 +182,146 @@ BwdWorkspace bwd_layout(int64_t BH, int N, int nb) {
     return w;
 }
 
+// ------------------------------------------------------- rotary positions, cache
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Strides of a [B, H, n, d] tensor read as 16-byte vectors: not negative, multiples of 8.
+int check_strides(const int64_t *s) {
+    for (int i = 0; i < 3; ++i) {
+        if (s[i] < 0) return FVATTN_ERR_INVALID_ARG;
+        if (s[i] % 8) return FVATTN_ERR_ALIGNMENT;
+    }
+    return FVATTN_OK;
+}
+
+// The same for a tensor that is written: its rows must not overlap.  Taken from the
+// smallest stride up, each dimension steps over all that the ones before it cover.
+int check_out_strides(const int64_t *s, int64_t B, int64_t H, int64_t n, int d) {
+    const int rc = check_strides(s);
+    if (rc != FVATTN_OK) return rc;
+    int64_t st[3] = {s[0], s[1], s[2]}, ext[3] = {B, H, n};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (st[j] > st[j + 1]) {
+                std::swap(st[j], st[j + 1]);
+                std::swap(ext[j], ext[j + 1]);
+            }
+    int64_t covered = d;
+    for (int i = 0; i < 3; ++i) {
+        if (ext[i] == 1) continue;
+        if (st[i] < covered) return FVATTN_ERR_INVALID_ARG;
+        if (st[i] > (INT64_MAX - covered) / ext[i]) return FVATTN_ERR_INVALID_ARG;
+        covered = st[i] * (ext[i] - 1) + covered;
+    }
+    return FVATTN_OK;
+}
+
+// The frequencies of a rotation as the kernels take them.
+int make_rope(RopeParams *p, const double *inv_freq, const int32_t *pair_axis, int n_pairs, int n_axes, int pairing,
+              int d) {
+    if (!inv_freq || !pair_axis) return FVATTN_ERR_INVALID_ARG;
+    if (n_axes < 1 || n_pairs < 1 || n_pairs > d / 2 || (pairing != 0 && pairing != 1)) return FVATTN_ERR_INVALID_ARG;
+    if (n_axes > kMaxRopeAxes) return FVATTN_ERR_UNSUPPORTED;
+    if (pairing == 1 && n_pairs % 8) return FVATTN_ERR_UNSUPPORTED;
+    for (int j = 0; j < n_pairs; ++j) {
+        if (!std::isfinite(inv_freq[j]) || pair_axis[j] < 0 || pair_axis[j] >= n_axes) return FVATTN_ERR_INVALID_ARG;
+        p->turns[j] = inv_freq[j] / (2.0 * 3.14159265358979323846);
+        p->axis[j] = static_cast<uint8_t>(pair_axis[j]);
+    }
+    p->n_pairs = n_pairs;
+    p->n_axes = n_axes;
+    return FVATTN_OK;
+}
+
+int check_pool(const void *k_codes, const void *k_exp, const void *v_codes, const void *v_exp, int num_pages,
+               const void *table, int max_pages, int block) {
+    if (!k_codes || !k_exp || !v_codes || !v_exp || !table || num_pages < 1 || max_pages < 1)
+        return FVATTN_ERR_INVALID_ARG;
+    if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_exp) || !aligned4(v_exp) || !aligned4(table))
+        return FVATTN_ERR_ALIGNMENT;
+    if (static_cast<int64_t>(max_pages) * block >= (1LL << 30)) return FVATTN_ERR_UNSUPPORTED;
+    return FVATTN_OK;
+}
+
+constexpr int kPlanSms = 148;  // the work plan's bound: workspace sizes do not depend on the device
+
+int check_attend_shape(int B, int heads, int group, int M, int d, int block, int max_pages) {
+    if (B < 1 || heads < 1 || group < 1 || M < 1 || max_pages < 1) return FVATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (block != 64 && block != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (B > kMaxHeads || static_cast<int64_t>(max_pages) * block >= (1LL << 30)) return FVATTN_ERR_UNSUPPORTED;
+    if (attend_rows(group, M) >= (1LL << 24)) return FVATTN_ERR_UNSUPPORTED;
+    const int64_t bh = static_cast<int64_t>(B) * heads;
+    if (bh >= (1LL << 31) || bh * (ceil_div(static_cast<int64_t>(max_pages) * block, 64) + 1) >= (1LL << 31))
+        return FVATTN_ERR_UNSUPPORTED;
+    // work items and grid sizes stay in 31 bits
+    if (bh * attend_rows(group, M) >= (1LL << 31) || static_cast<int64_t>(B) * max_pages >= (1LL << 31) - 4096)
+        return FVATTN_ERR_UNSUPPORTED;
+    return FVATTN_OK;
+}
+
+struct CacheTilesWorkspace {
+    size_t counter, nan_first, zero_bytes, K, V, total;
+    int64_t cap;
+};
+
+CacheTilesWorkspace cache_tiles_layout(int64_t BH, int d, int block, int max_pages) {
+    CacheTilesWorkspace w{};
+    Carver c;
+    w.cap = static_cast<int64_t>(align_up(static_cast<size_t>(max_pages) * block, 128));
+    w.counter = c.take<int32_t>(64);
+    w.nan_first = c.take<int32_t>(static_cast<size_t>(BH) * d);
+    w.zero_bytes = c.off;
+    w.K = c.take<uint16_t>(static_cast<size_t>(BH) * w.cap * d);
+    w.V = c.take<uint16_t>(static_cast<size_t>(BH) * w.cap * d);
+    w.total = align_up(c.off, 256);
+    return w;
+}
+
+// More than 32 rows: the pages as bf16, then 128-row tiles over them.
+int attend_tiles(const AttendLaunch &a, cudaStream_t s) {
+    const int64_t BH = static_cast<int64_t>(a.B) * a.pool.heads;
+    const int d = a.pool.d;
+    const CacheTilesWorkspace w = cache_tiles_layout(BH, d, a.pool.block, a.pool.max_pages);
+    char *ws = static_cast<char *>(a.workspace);
+    CUtensorMap mk, mv;
+    if (!make_map(&mk, ws + w.K, BH, static_cast<int>(w.cap), d, 128) ||
+        !make_map(&mv, ws + w.V, BH, static_cast<int>(w.cap), d, 128))
+        return FVATTN_ERR_CUDA;
+    int32_t *nan_first = reinterpret_cast<int32_t *>(ws + w.nan_first);
+    int rc = from_cuda(cudaMemsetAsync(ws, 0, w.zero_bytes, s));
+    if (rc != FVATTN_OK) return rc;
+    if ((rc = from_cuda(launch_cache_expand(a, w.cap, ws + w.K, ws + w.V, nan_first, s))) != FVATTN_OK) return rc;
+    CacheTiles ct{};
+    ct.lens = a.lens;
+    ct.new_lens = a.new_lens;
+    ct.nan_first = nan_first;
+    ct.heads = a.pool.heads;
+    ct.group = a.group;
+    ct.M = a.M;
+    ct.rows = static_cast<int>(attend_rows(a.group, a.M));
+    ct.row_tiles = static_cast<int>(ceil_div(ct.rows, 128));
+    ct.causal = a.causal;
+    ct.cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
+    ct.q_b = a.q_b, ct.q_h = a.q_h, ct.q_n = a.q_n;
+    ct.o_b = a.o_b, ct.o_h = a.o_h, ct.o_n = a.o_n;
+    AttnLaunch l{};
+    l.Q = a.Q;
+    l.tmap_k = &mk;
+    l.tmap_v = &mv;
+    l.n_items = static_cast<int>(BH * ct.row_tiles);
+    l.work_counter = reinterpret_cast<int *>(ws + w.counter);
+    l.N = static_cast<int>(w.cap);
+    l.nb = static_cast<int>(w.cap / 128);
+    l.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+    l.O = a.O;
+    l.LSE = a.LSE;
+    l.dev_status = a.dev_status;
+    l.sms = a.sms;
+    return from_cuda(launch_cache_tiles(l, ct, d, s));
+}
+
 // st[2] keeps the first error of st[0] (routing) and st[1] (attention) over successive calls.
 __global__ void status_merge_kernel(int32_t *st) {
     if (st[2] == 0) st[2] = st[0] != 0 ? st[0] : st[1];
@@ -199,6 +341,7 @@ const char *fvattn_status_string(int status) {
         case FVATTN_ERR_CUDA: return "CUDA error";
         case FVATTN_ERR_BAD_CSR: return "malformed CSR block mask";
         case FVATTN_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+        case FVATTN_ERR_BAD_PAGE: return "page table entry, length or count out of range";
         default: return "unknown status";
     }
 }
@@ -682,6 +825,132 @@ int fvattn_attention_host(const void *hQ, const void *hK, const void *hV, int B,
     if (rc != FVATTN_OK) return rc;
     if (rs1 != FVATTN_OK || rs2 != FVATTN_OK || rs3 != FVATTN_OK) return FVATTN_ERR_CUDA;
     return st;
+}
+
+int fvattn_rope(const void *Q, const int64_t *q_strides, void *Qr, const int64_t *qr_strides, int q_heads,
+                const void *K, const int64_t *k_strides, void *Kr, const int64_t *kr_strides, int k_heads, int B,
+                int N, int d, const int32_t *pos, int64_t pos_batch_stride, const double *inv_freq,
+                const int32_t *pair_axis, int n_pairs, int n_axes, int pairing, int inverse, fvattn_stream_t stream) {
+    if (B < 1 || N < 1 || q_heads < 1 || k_heads < 0) return FVATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (!Q || !Qr || !q_strides || !qr_strides || !pos) return FVATTN_ERR_INVALID_ARG;
+    if (k_heads > 0 && (!K || !Kr || !k_strides || !kr_strides)) return FVATTN_ERR_INVALID_ARG;
+    if (k_heads == 0 && (K || Kr)) return FVATTN_ERR_INVALID_ARG;
+    if (inverse != 0 && inverse != 1) return FVATTN_ERR_INVALID_ARG;
+    if (B > 65535 || q_heads > 65535 - k_heads) return FVATTN_ERR_UNSUPPORTED;
+    RopeParams p{};
+    int rc = make_rope(&p, inv_freq, pair_axis, n_pairs, n_axes, pairing, d);
+    if (rc != FVATTN_OK) return rc;
+    if (pos_batch_stride != 0 && pos_batch_stride != static_cast<int64_t>(N) * n_axes) return FVATTN_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(Qr) || !aligned16(K) || !aligned16(Kr) || !aligned4(pos))
+        return FVATTN_ERR_ALIGNMENT;
+    if ((rc = check_strides(q_strides)) != FVATTN_OK) return rc;
+    if ((rc = check_out_strides(qr_strides, B, q_heads, N, d)) != FVATTN_OK) return rc;
+    RopeTensor q{Q, Qr, q_strides[0], q_strides[1], q_strides[2], qr_strides[0], qr_strides[1], qr_strides[2], q_heads};
+    RopeTensor k{};
+    if (k_heads > 0) {
+        if ((rc = check_strides(k_strides)) != FVATTN_OK) return rc;
+        if ((rc = check_out_strides(kr_strides, B, k_heads, N, d)) != FVATTN_OK) return rc;
+        k = RopeTensor{K, Kr, k_strides[0], k_strides[1], k_strides[2], kr_strides[0], kr_strides[1], kr_strides[2],
+                       k_heads};
+    }
+    DeviceInfo info;
+    if ((rc = check_device()) != FVATTN_OK) return rc;
+    if (!device_info(&info)) return FVATTN_ERR_CUDA;
+    return from_cuda(launch_rope(q, k, pos, pos_batch_stride, B, N, d, pairing == 1, inverse == 1, p, info.sms,
+                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, const int64_t *v_strides, int B,
+                        int heads, int T, int d, int block, uint8_t *k_codes, int32_t *k_exp, uint8_t *v_codes,
+                        int32_t *v_exp, int num_pages, const int32_t *page_table, int max_pages, const int32_t *start,
+                        const int32_t *new_lens, const int32_t *pos, int64_t pos_batch_stride, const double *inv_freq,
+                        const int32_t *pair_axis, int n_pairs, int n_axes, int pairing, int32_t *dev_status,
+                        fvattn_stream_t stream) {
+    if (B < 1 || heads < 1 || T < 1) return FVATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (block != 64 && block != 128) return FVATTN_ERR_UNSUPPORTED;
+    if (!K || !V || !k_strides || !v_strides || !start || !dev_status) return FVATTN_ERR_INVALID_ARG;
+    int rc = check_pool(k_codes, k_exp, v_codes, v_exp, num_pages, page_table, max_pages, block);
+    if (rc != FVATTN_OK) return rc;
+    if (!aligned16(K) || !aligned16(V) || !aligned4(start) || !aligned4(new_lens) || !aligned4(pos) ||
+        !aligned4(dev_status))
+        return FVATTN_ERR_ALIGNMENT;
+    if ((rc = check_strides(k_strides)) != FVATTN_OK || (rc = check_strides(v_strides)) != FVATTN_OK) return rc;
+    AppendLaunch a{};
+    if (pos) {
+        if ((rc = make_rope(&a.rope, inv_freq, pair_axis, n_pairs, n_axes, pairing, d)) != FVATTN_OK) return rc;
+        if (pos_batch_stride != 0 && pos_batch_stride != static_cast<int64_t>(T) * n_axes)
+            return FVATTN_ERR_INVALID_ARG;
+    }
+    const int64_t bh = static_cast<int64_t>(B) * heads;
+    if (bh >= (1LL << 30) || bh * 2 * max_touched_pages(T, block) + 1 >= (1LL << 31)) return FVATTN_ERR_UNSUPPORTED;
+    if ((rc = check_device()) != FVATTN_OK) return rc;
+    a.pool = CachePool{k_codes, v_codes, k_exp, v_exp, num_pages, heads, block, d, page_table, max_pages};
+    a.K = K;
+    a.V = V;
+    a.k_b = k_strides[0], a.k_h = k_strides[1], a.k_n = k_strides[2];
+    a.v_b = v_strides[0], a.v_h = v_strides[1], a.v_n = v_strides[2];
+    a.B = B;
+    a.T = T;
+    a.start = start;
+    a.new_lens = new_lens;
+    a.pos = pos;
+    a.pos_b = pos_batch_stride;
+    a.half = pos && pairing == 1;
+    a.dev_status = dev_status;
+    return from_cuda(launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block, int max_pages) {
+    if (check_attend_shape(B, heads, group, M, d, block, max_pages) != FVATTN_OK) return 0;
+    if (attend_few_rows(group, M)) return attend_few_workspace(B, heads, group, M, d, block, max_pages, kPlanSms);
+    return cache_tiles_layout(static_cast<int64_t>(B) * heads, d, block, max_pages).total;
+}
+
+int fvattn_cache_attend(const void *Q, const int64_t *q_strides, int B, int heads, int group, int M, int d, int block,
+                        const uint8_t *k_codes, const int32_t *k_exp, const uint8_t *v_codes, const int32_t *v_exp,
+                        int num_pages, const int32_t *page_table, int max_pages, const int32_t *lens,
+                        const int32_t *new_lens, int causal, void *O, const int64_t *o_strides, float *LSE,
+                        void *workspace, size_t ws_bytes, int32_t *dev_status, fvattn_stream_t stream) {
+    int rc = check_attend_shape(B, heads, group, M, d, block, max_pages);
+    if (rc != FVATTN_OK) return rc;
+    if (!Q || !q_strides || !lens || !O || !o_strides || !LSE || !workspace || !dev_status)
+        return FVATTN_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return FVATTN_ERR_INVALID_ARG;
+    if ((rc = check_pool(k_codes, k_exp, v_codes, v_exp, num_pages, page_table, max_pages, block)) != FVATTN_OK)
+        return rc;
+    if (!aligned16(Q) || !aligned16(O) || !aligned16(workspace) || !aligned4(lens) || !aligned4(new_lens) ||
+        !aligned4(LSE) || !aligned4(dev_status))
+        return FVATTN_ERR_ALIGNMENT;
+    if ((rc = check_strides(q_strides)) != FVATTN_OK) return rc;
+    if ((rc = check_out_strides(o_strides, B, static_cast<int64_t>(heads) * group, M, d)) != FVATTN_OK) return rc;
+    if (ws_bytes < fvattn_cache_attend_workspace_bytes(B, heads, group, M, d, block, max_pages))
+        return FVATTN_ERR_CAPACITY;
+    DeviceInfo info;
+    if ((rc = check_device()) != FVATTN_OK) return rc;
+    if (!device_info(&info)) return FVATTN_ERR_CUDA;
+    AttendLaunch a{};
+    a.pool = CachePool{const_cast<uint8_t *>(k_codes), const_cast<uint8_t *>(v_codes), const_cast<int32_t *>(k_exp),
+                       const_cast<int32_t *>(v_exp), num_pages, heads, block, d, page_table, max_pages};
+    a.Q = Q;
+    a.O = O;
+    a.LSE = LSE;
+    a.q_b = q_strides[0], a.q_h = q_strides[1], a.q_n = q_strides[2];
+    a.o_b = o_strides[0], a.o_h = o_strides[1], a.o_n = o_strides[2];
+    a.B = B;
+    a.group = group;
+    a.M = M;
+    a.lens = lens;
+    a.new_lens = new_lens;
+    a.causal = causal;
+    a.dev_status = dev_status;
+    a.workspace = workspace;
+    a.sms = info.sms < kPlanSms ? info.sms : kPlanSms;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (attend_few_rows(group, M)) return from_cuda(launch_attend_few(a, s));
+    a.sms = info.sms;
+    return attend_tiles(a, s);
 }
 
 }  // extern "C"

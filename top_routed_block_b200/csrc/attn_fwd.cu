@@ -70,6 +70,7 @@
 #include <math_constants.h>
 
 #include "attn_fwd.cuh"
+#include "cache_index.h"
 #include "common.cuh"
 #include "ptx_sm100.cuh"
 
@@ -167,6 +168,44 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 // sums of degenerate blocks finite).
 __device__ __forceinline__ float pow2_scale(float x, int e) { return ldexpf(x, max(-200, min(e, 126))); }
 
+// ------------------------------------------------- cached keys (CacheTiles)
+// Row r of item `item`: one query token of one query head, and what it sees.
+struct CacheRow {
+    bool valid;          // a row of the head's, and its token one of the sequence's new ones
+    int limit;           // it sees cached tokens [0, limit)
+    int64_t q_at, o_at;  // its first element in Q and O
+    int64_t lse_at;
+};
+
+__device__ __forceinline__ CacheRow cache_row(const CacheTiles &ct, int item, int r) {
+    const int bh = item / ct.row_tiles, row = (item % ct.row_tiles) * kRowsM + r;
+    const int b = bh / ct.heads, h = bh % ct.heads;
+    const int len = static_cast<int>(clamp_len(__ldg(ct.lens + b), ct.cap));
+    const int n_new = ct.new_lens ? static_cast<int>(clamp_len(__ldg(ct.new_lens + b), ct.M)) : ct.M;
+    const int m = row % ct.M;
+    CacheRow c;
+    c.valid = row < ct.rows && m < n_new;
+    const int64_t hq = c.valid ? h * ct.group + row / ct.M : 0, tok = c.valid ? m : 0;
+    c.limit = !c.valid ? 0 : ct.causal ? static_cast<int>(clamp_len(static_cast<int64_t>(len) - n_new + m + 1, len)) : len;
+    c.q_at = b * ct.q_b + hq * ct.q_h + tok * ct.q_n;
+    c.o_at = b * ct.o_b + hq * ct.o_h + tok * ct.o_n;
+    c.lse_at = (static_cast<int64_t>(b) * ct.heads * ct.group + hq) * ct.M + tok;
+    return c;
+}
+
+// Key tiles an item walks: up to the last token that one of its rows sees.
+__device__ __forceinline__ int cache_tiles_of(const CacheTiles &ct, int item) {
+    const int bh = item / ct.row_tiles, row0 = (item % ct.row_tiles) * kRowsM;
+    const int b = bh / ct.heads;
+    const int len = static_cast<int>(clamp_len(__ldg(ct.lens + b), ct.cap));
+    const int n_new = ct.new_lens ? static_cast<int>(clamp_len(__ldg(ct.new_lens + b), ct.M)) : ct.M;
+    if (n_new == 0) return 0;
+    const int row1 = min(row0 + kRowsM, ct.rows) - 1;
+    const int last = row0 / ct.M == row1 / ct.M ? min(row1 % ct.M, n_new - 1) : n_new - 1;
+    const int64_t sees = ct.causal ? clamp_len(static_cast<int64_t>(len) - n_new + last + 1, len) : len;
+    return static_cast<int>((sees + kKT - 1) / kKT);
+}
+
 // ------------------------------------------------------------- block-64 pairs
 // Pair i of head bh: query blocks 2i (row A) and 2i+1 (row B, absent when nb is
 // odd and i is the last pair).  The 32 lanes of a warp set one bit per selected
@@ -230,7 +269,9 @@ __device__ int pair_union(const uint32_t *bm, int nb, uint16_t *out, int lane) {
     return __shfl_sync(0xffffffffu, inc, 31);
 }
 
-template <int D, int BS, bool F8>
+// CACHE: dense attention over the expanded pages of an 8-bit cache (CacheTiles) instead
+// of the key blocks of a CSR row; an item is 128 query rows of one (sequence, key head).
+template <int D, int BS, bool F8, bool CACHE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     sparse_attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                            const unsigned char *__restrict__ Qg, const int32_t *__restrict__ row_ptr,
@@ -238,7 +279,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                            int *__restrict__ work_counter, int N, int nb, int causal, float scale_log2,
                            __nv_bfloat16 *__restrict__ O, float *__restrict__ LSE, int32_t *dev_status,
                            int test_stall, long long *__restrict__ cta_busy_ns, const int32_t *__restrict__ q_exp,
-                           const int32_t *__restrict__ k_exp, const int32_t *__restrict__ v_exp) {
+                           const int32_t *__restrict__ k_exp, const int32_t *__restrict__ v_exp,
+                           const __grid_constant__ CacheTiles ct) {
+    static_assert(!CACHE || (BS == kRowsM && !F8), "the cache's tiles are 128 bf16 keys");
     using C = Cfg<D, BS, F8>;
     constexpr int NST = C::NST;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -249,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // pairs only: the two union slots and the bitmaps
     uint16_t *uni = reinterpret_cast<uint16_t *>(ring + C::TILE_BYTES + 512);
     uint32_t *bmap = reinterpret_cast<uint32_t *>(ring + C::TILE_BYTES + 512 + 2 * kUnionCap * 2);
-    const int ipb = C::PAIR ? (nb + 1) >> 1 : nb;  // items per head
+    const int ipb = CACHE ? ct.row_tiles : C::PAIR ? (nb + 1) >> 1 : nb;  // items per head
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -371,9 +414,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             bool ok = true;
             while (ok) {
                 const int idx = atomicAdd(work_counter, 1);
-                const int rw = (idx < n_items) ? order[idx] : -1;
+                const int rw = (idx < n_items) ? (CACHE ? idx : order[idx]) : -1;
                 int4 item = make_int4(-1, 0, 0, 0);
-                if (rw >= 0) {
+                if (CACHE && rw >= 0) {
+                    item = make_int4(rw, 0, cache_tiles_of(ct, rw), idx + 1);
+                } else if (rw >= 0) {
                     int c = row_ptr[rw + 1] - row_ptr[rw];
                     if (c < 0) {
                         record_error(dev_status, FVATTN_ERR_BAD_CSR);
@@ -387,13 +432,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 mbar_arrive(&bar->sched_full[k]);
                 ++it;
                 if (rw < 0) break;
-                const int bh = rw / nb;
+                const int bh = rw / ipb;
                 int prev = -1;
-                int kblk_next = item.z > 0 ? __ldg(col_idx + item.y) : 0;  // loaded one tile ahead
+                int kblk_next = !CACHE && item.z > 0 ? __ldg(col_idx + item.y) : 0;  // loaded one tile ahead
                 for (int j = 0; j < item.z && ok; ++j) {
-                    int kblk = kblk_next;
-                    if (j + 1 < item.z) kblk_next = __ldg(col_idx + item.y + j + 1);
-                    if (kblk >= 0 && kblk < nb && kblk > prev) {
+                    int kblk = CACHE ? j : kblk_next;
+                    if (!CACHE && j + 1 < item.z) kblk_next = __ldg(col_idx + item.y + j + 1);
+                    if (CACHE || (kblk >= 0 && kblk < nb && kblk > prev)) {
                         prev = kblk;
                     } else {  // skipped by the softmax; any in-range tile will do
                         record_error(dev_status, FVATTN_ERR_BAD_CSR);
@@ -543,8 +588,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         auto load_q = [&](const int4 &itm) {
             const int64_t bhq = itm.x / ipb;
             const int tq = (itm.x % ipb) * kRowsM + r;
-            const bool in = tq < N;
-            const uint4 *src = reinterpret_cast<const uint4 *>(Qg + (bhq * N + (in ? tq : 0)) * (D * C::EB));
+            const CacheRow crow = CACHE ? cache_row(ct, itm.x, r) : CacheRow{};
+            const bool in = CACHE ? crow.valid : tq < N;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                CACHE ? Qg + crow.q_at * C::EB : Qg + (bhq * N + (in ? tq : 0)) * (D * C::EB));
             const uint32_t tQ = tmem + lane_base + ((qn & 1) ? C::T_Q1 : C::T_Q0);
 #pragma unroll
             for (int c0 = 0; c0 < static_cast<int>(C::Q_COLS); c0 += 32) {
@@ -582,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 float m = -CUDART_INF_F, l = 0.0f;
                 int prev = -1;
                 // rows: the next tile's key block, loaded one tile ahead
-                int kblk_next = (!C::PAIR && count > 0) ? __ldg(col_idx + start) : 0;
+                int kblk_next = (!CACHE && !C::PAIR && count > 0) ? __ldg(col_idx + start) : 0;
+                const CacheRow crow = CACHE ? cache_row(ct, item.x, r) : CacheRow{};
                 // e4m3 operands: the row's Q exponent, the running V reference exponent E
                 const int eq = (F8 && qb < nb) ? __ldg(q_exp + bh * nb + qb) : 0;
                 int e_ref = 0;
@@ -598,6 +646,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             kb[h] = e >= 0 ? (e >> 2) : -1;
                             mine[h] = e >= 0 && ((e >> half) & 1);
                         }
+                    } else if constexpr (CACHE) {
+                        kb[0] = j;
+                        mine[0] = true;
                     } else {
                         kb[0] = kblk_next;
                         if (j + 1 < count) kblk_next = __ldg(col_idx + start + j + 1);
@@ -612,12 +663,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     bool e_up = false;
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h) {
-                        const bool valid = kb[h] >= 0 && kb[h] < nb && kb[h] > prev;
+                        const bool valid = CACHE || (kb[h] >= 0 && kb[h] < nb && kb[h] > prev);
                         if (valid) prev = kb[h];
                         mine[h] = mine[h] && valid;
                         const int key0 = kb[h] * BS;
-                        lim[h] = mine[h] ? min(BS, N - key0) : 0;
-                        if (causal) lim[h] = min(lim[h], t_row - key0 + 1);
+                        lim[h] = mine[h] ? min(BS, (CACHE ? crow.limit : N) - key0) : 0;
+                        if (!CACHE && causal) lim[h] = min(lim[h], t_row - key0 + 1);
                         sc[h] = scale_log2;
                         ev[h] = 0;
                         if (F8 && mine[h]) {
@@ -678,6 +729,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         uint64_t sc2[C::HALVES];
 #pragma unroll
                         for (int h = 0; h < C::HALVES; ++h) sc2[h] = f32x2_pack(sc[h], sc[h]);
+                        if constexpr (CACHE) {
+                            // scores past 2^20: the reference maximum is a rounded product, and an
+                            // unrounded s * scale less it may be far from zero at the maximum itself;
+                            // round every product as the maximum was (a page's scale can be any power
+                            // of two, so that such scores are finite here)
+                            if (__any_sync(0xffffffffu, fabsf(neg_m) > 1048576.0f)) {
+#pragma unroll
+                                for (int c = 0; c < kKT; ++c) v[c] = __float_as_uint(__fmul_rn(__uint_as_float(v[c]), sc[0]));
+                                sc2[0] = f32x2_pack(1.0f, 1.0f);
+                            }
+                        }
                         const uint64_t nm2 = f32x2_pack(neg_m, neg_m);
                         uint64_t acc2[2] = {0ull, 0ull};
 #pragma unroll
@@ -776,9 +838,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (!mbar_wait(&bar->o_full, on & 1, abort_flag, dev_status)) break;
                 ++on;
                 tc_fence_after();
-                const bool row_ok = t_row < N;
-                const float inv_l = (l > 0.0f) ? (F8 ? pow2_scale(1.0f / l, e_ref) : 1.0f / l) : 0.0f;
-                __nv_bfloat16 *orow = O + (bh * N + t_row) * D;
+                const bool row_ok = CACHE ? crow.valid : t_row < N;
+                const float inv_l = (CACHE ? l != 0.0f : l > 0.0f) ? (F8 ? pow2_scale(1.0f / l, e_ref) : 1.0f / l) : 0.0f;
+                __nv_bfloat16 *orow = O + (CACHE ? crow.o_at : (bh * N + t_row) * D);
                 const uint32_t tO = tmem + lane_base + C::T_O;
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -794,6 +856,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                     for (int c = 0; c < 32; c += 2)
                         pkk[c >> 1] = pack_bf16(__uint_as_float(o[c]) * inv_l, __uint_as_float(o[c + 1]) * inv_l);
+                    if constexpr (CACHE) {
+                        // a channel whose first NaN value this row sees (the copy of V has none)
+                        const int4 *nf = reinterpret_cast<const int4 *>(ct.nan_first + bh * D + c0);
+                        const int seen = 0x7fffffff - crow.limit;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int4 f = __ldg(nf + q);
+                            if (f.x > seen) pkk[2 * q] |= 0x7fffu;
+                            if (f.y > seen) pkk[2 * q] |= 0x7fff0000u;
+                            if (f.z > seen) pkk[2 * q + 1] |= 0x7fffu;
+                            if (f.w > seen) pkk[2 * q + 1] |= 0x7fff0000u;
+                        }
+                    }
                     if (row_ok) {
                         uint4 *dst = reinterpret_cast<uint4 *>(orow + c0);
 #pragma unroll
@@ -801,7 +876,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             dst[q] = make_uint4(pkk[4 * q], pkk[4 * q + 1], pkk[4 * q + 2], pkk[4 * q + 3]);
                     }
                 }
-                if (row_ok)
+                if (row_ok && CACHE)  // a NaN sum stays one
+                    LSE[crow.lse_at] = (l == 0.0f) ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+                else if (row_ok)
                     LSE[bh * N + t_row] = (l > 0.0f) ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
                 tc_fence_before();
                 __syncwarp();
@@ -969,9 +1046,9 @@ cudaError_t launch_natural_order(int64_t n, int32_t *order, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <int D, int BS, bool F8>
-static cudaError_t launch_t(const AttnLaunch &a, cudaStream_t stream) {
-    auto kern = sparse_attn_fwd_kernel<D, BS, F8>;
+template <int D, int BS, bool F8, bool CACHE = false>
+static cudaError_t launch_t(const AttnLaunch &a, cudaStream_t stream, const CacheTiles &ct = CacheTiles{}) {
+    auto kern = sparse_attn_fwd_kernel<D, BS, F8, CACHE>;
     // Checked once per instantiation: the number of resident CTAs per SM sizes the
     // persistent grid.
     static int per_sm = 0;  // 0 unknown, > 0 resident CTAs per SM, < 0 not launchable
@@ -999,7 +1076,7 @@ static cudaError_t launch_t(const AttnLaunch &a, cudaStream_t stream) {
     kern<<<grid, kThreads, Cfg<D, BS, F8>::SMEM_BYTES, stream>>>(
         *a.tmap_k, *a.tmap_v, static_cast<const unsigned char *>(a.Q), a.row_ptr, a.col_idx, a.order, a.n_items,
         a.work_counter, a.N, a.nb, a.causal, a.scale_log2, static_cast<__nv_bfloat16 *>(a.O), a.LSE, a.dev_status,
-        a.test_stall, a.cta_busy_ns, a.q_exp, a.k_exp, a.v_exp);
+        a.test_stall, a.cta_busy_ns, a.q_exp, a.k_exp, a.v_exp, ct);
     return cudaGetLastError();
 }
 
@@ -1013,6 +1090,11 @@ cudaError_t launch_sparse_attn(const AttnLaunch &a, int d, int bs, cudaStream_t 
 cudaError_t launch_sparse_attn_fp8(const AttnLaunch &a, int bs, cudaStream_t stream) {
     if (bs == 128) return launch_t<128, 128, true>(a, stream);
     return launch_t<128, 64, true>(a, stream);
+}
+
+cudaError_t launch_cache_tiles(const AttnLaunch &a, const CacheTiles &ct, int d, cudaStream_t stream) {
+    if (d == 128) return launch_t<128, 128, false, true>(a, stream, ct);
+    return launch_t<64, 128, false, true>(a, stream, ct);
 }
 
 }  // namespace fvattn

@@ -29,6 +29,18 @@ struct AttnLaunch {
     const int32_t *q_exp, *k_exp, *v_exp;
 };
 
+// Dense attention of many new query rows per sequence over cached keys and values that
+// lie expanded as bf16 [B * heads, cap, d] (the tensor maps of AttnLaunch, boxes of 128
+// tokens): what the kernel needs instead of a CSR.  Rows of one key head are its `group`
+// query heads times M new tokens; an item is 128 of them.
+struct CacheTiles {
+    const int32_t *lens, *new_lens;  // per sequence: cached tokens, new ones (null: all M)
+    const int32_t *nan_first;        // [B * heads, d]: 2^31 - 1 - first token whose V was NaN there, 0 none
+    int heads, group, M, rows, row_tiles, causal;
+    int64_t cap;
+    int64_t q_b, q_h, q_n, o_b, o_h, o_n;  // strides of Q and O, in elements
+};
+
 int attn_smem_bytes(int d, int bs);
 // Work items of the attention kernel: the CSR rows (query blocks of every head) at
 // block 128, the pairs of neighbouring rows at block 64.
@@ -45,6 +57,8 @@ cudaError_t launch_item_order(const int32_t *row_ptr, int64_t BH, int nb, int32_
 cudaError_t launch_natural_order(int64_t n, int32_t *order, cudaStream_t stream);
 int attn_ctas_per_sm();  // resident CTAs per SM the launch grid is sized for
 cudaError_t launch_sparse_attn(const AttnLaunch &a, int d, int bs, cudaStream_t stream);
+// Cached keys: bs = 128; n_items = B * heads * row_tiles, `order` and the CSR unused.
+cudaError_t launch_cache_tiles(const AttnLaunch &a, const CacheTiles &ct, int d, cudaStream_t stream);
 // e4m3 operands (tmap_* over uint8 codes), d = 128, bs in {64, 128}.
 cudaError_t launch_sparse_attn_fp8(const AttnLaunch &a, int bs, cudaStream_t stream);
 

@@ -1,0 +1,85 @@
+// cache.cuh -- internal interface of the paged 8-bit key/value cache: appending
+// (cache_append.cu) and attention (cache_attend.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "cache_index.h"
+#include "rope.cuh"
+
+namespace fvattn {
+
+// The pool: page p, head h, slot s, channel c at ((p * heads + h) * block + s) * d + c.
+struct CachePool {
+    uint8_t *k, *v;        // e4m3 codes
+    int32_t *ke, *ve;      // power-of-two scale exponents [num_pages, heads]
+    int num_pages, heads, block, d;
+    const int32_t *table;  // [B, max_pages]
+    int max_pages;
+};
+
+// Exponent of a page that holds only zeros: below what any fp32 value asks for, so that
+// the next tokens set the scale.
+constexpr int kZeroPageExp = -160;
+
+struct AppendLaunch {
+    CachePool pool;
+    const void *K, *V;  // bf16 [B, heads, T, d] with strides
+    int64_t k_b, k_h, k_n, v_b, v_h, v_n;
+    int B, T;
+    const int32_t *start, *new_lens;  // new_lens may be null: all T
+    const int32_t *pos;               // null: no rotation
+    int64_t pos_b;
+    bool half;
+    RopeParams rope;
+    int32_t *dev_status;
+};
+
+cudaError_t launch_cache_append(const AppendLaunch &a, cudaStream_t stream);
+
+struct AttendLaunch {
+    CachePool pool;
+    const void *Q;  // bf16 [B, heads * group, M, d] with strides
+    void *O;
+    float *LSE;     // [B, heads * group, M]
+    int64_t q_b, q_h, q_n, o_b, o_h, o_n;
+    int B, group, M;
+    const int32_t *lens, *new_lens;  // new_lens may be null: all M
+    int causal;
+    int32_t *dev_status;
+    void *workspace;
+    int sms;
+};
+
+// Rows of one key head: its query heads times M new tokens.
+inline int64_t attend_rows(int group, int M) { return static_cast<int64_t>(group) * M; }
+// Whether the call takes the few-rows kernel (else the pages are expanded and the tensor
+// cores' 128-row tiles run over them).
+bool attend_few_rows(int group, int M);
+size_t attend_few_workspace(int B, int heads, int group, int M, int d, int block, int max_pages, int sms);
+cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream);
+// Pages of every sequence as bf16 K and V [B * heads, cap, d] (zeros from the sequence's end
+// to the next multiple of 128 tokens), and the calls' device checks.  nan_first: int32 [B * heads,
+// d], zeroed before; gets 2^31 - 1 - t for the first token t whose V is NaN in that channel.
+cudaError_t launch_cache_expand(const AttendLaunch &a, int64_t cap, void *K, void *V, int32_t *nan_first,
+                                cudaStream_t stream);
+
+#ifdef __CUDACC__
+
+// x * 2^e for |e| up to 252: two exact factors (a single 2^e may lie outside fp32).  Exact
+// unless the result is subnormal.
+__device__ __forceinline__ float scale_pow2(float x, int e) {
+    const int h = e / 2;
+    return x * __int_as_float((h + 127) << 23) * __int_as_float((e - h + 127) << 23);
+}
+__device__ __forceinline__ int clamp_exp(int e) { return max(-250, min(e, 250)); }
+
+// Whether any of the four e4m3 codes of w is a NaN (0x7F or 0xFF).
+__device__ __forceinline__ bool any_nan_e4m3(uint32_t w) {
+    return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
+
+#endif
+
+}  // namespace fvattn
