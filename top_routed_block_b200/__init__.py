@@ -435,9 +435,6 @@ def fvattn_sparse_fwd_noalloc(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 
 # ------------------------------------------------------- rotary positions, 8-bit cache
 
-PAIRINGS = {"interleaved": 0, "half": 1}
-
-
 class RopeAxes(NamedTuple):
     """What turns a head's channel pairs: per pair an angle per unit of position and the
     axis (column of the positions) it goes by; ``pairing`` says which two channels
@@ -465,72 +462,33 @@ def grid_positions(T: int, H: int, W: int, *, first_frame: int = 0, device="cuda
     return torch.stack(torch.meshgrid(t, y, x, indexing="ij"), -1).reshape(-1, 3).contiguous()
 
 
-_Strides = ctypes.c_int64 * 3
+_native = None
 
 
-def _heads_tensor(t: torch.Tensor, what: str):
-    """(B, H, n, d) and the strides of a bf16 CUDA tensor whose channels are contiguous."""
-    if t.dim() != 4 or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA bf16 tensor [B, H, n, d]")
-    shape, st = t.shape, t.stride()
-    if st[3] != 1:
-        raise ValueError(f"{what}: the channels of a head must be contiguous")
-    return tuple(shape), _Strides(*(0 if n == 1 else x for n, x in zip(shape[:3], st)))
+def _native_calls():
+    """The compiled module behind the calls below (built with the library)."""
+    global _native
+    if _native is None:
+        load_library()
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise FvattnError(FVATTN_ERR_UNSUPPORTED, f"_binding.so not built ({e}); "
+                              "run python -m top_routed_block_b200._build") from e
+        _native = m
+    return _native
 
 
-def _int32(t: torch.Tensor | None, shape, what: str, device) -> None:
-    if t is None:
-        return
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{what}: expected a contiguous int32 tensor {list(shape)} on {device}")
-
-
-def _status_word(t: torch.Tensor, device) -> None:
-    if t.dtype != torch.int32 or t.numel() < 1 or t.device != device:
-        raise ValueError(f"dev_status: expected an int32 tensor on {device}")
-
-
-class _On:
-    """A call on ``device``: makes it current if it is not, and gives the stream (the
-    caller's, or the device's current one).  Tensors made inside for a stream that is
-    not current are kept from reuse until that stream has passed them."""
-
-    def __init__(self, device: torch.device, stream):
-        self.switch = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-        self.device, self.other = device, stream
-
-    def __enter__(self):
-        if self.switch is not None:
-            self.switch.__enter__()
-        self.stream = int((self.other or torch.cuda.current_stream(self.device)).cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        if self.switch is not None:
-            self.switch.__exit__(*exc)
-
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
-
-
-def _rope_args(rope: RopeAxes, positions: torch.Tensor, B: int, n: int, device):
-    """(arrays kept alive, C arguments from the positions to the pairing)."""
-    import numpy as np
-    freq = np.ascontiguousarray(rope.inv_freq, dtype=np.float64)
-    axis = np.ascontiguousarray(rope.pair_axis, dtype=np.int32)
-    if freq.ndim != 1 or axis.shape != freq.shape:
-        raise ValueError("rope: inv_freq and pair_axis are two lists of the same length")
-    if rope.pairing not in PAIRINGS:
-        raise ValueError(f"rope: pairing is one of {sorted(PAIRINGS)}")
-    if positions.dim() not in (2, 3):
-        raise ValueError("positions: expected [n, axes] or [B, n, axes]")
-    axes = positions.shape[-1]
-    _int32(positions, (n, axes) if positions.dim() == 2 else (B, n, axes), "positions", device)
-    return (freq, axis), (positions.data_ptr(), 0 if positions.dim() == 2 else n * axes, freq.ctypes.data,
-                          axis.ctypes.data, freq.size, axes, PAIRINGS[rope.pairing])
+def _on_stream(stream, f, *args):
+    """f(*args) with `stream` current, so that what it allocates belongs to that stream.  Its results
+    are kept from reuse until the caller's own stream has passed them too."""
+    before = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        r = f(*args)
+    for t in r if isinstance(r, tuple) else (r,):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(before)
+    return r
 
 
 def fvattn_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, rope: RopeAxes, *,
@@ -540,32 +498,12 @@ def fvattn_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor
     contiguous channels, e.g. ``x.view(B, N, H, d).transpose(1, 2)`` of a projection; K may
     be None).  positions: int32 [N, axes] or [B, N, axes].  Returns the turned Q and K,
     contiguous unless out_q / out_k are given (which may be Q and K themselves)."""
-    lib = load_library()
-    (B, H, N, d), qs = _heads_tensor(Q, "Q")
-    dev = Q.device
-    if K is None and out_k is not None:
-        raise ValueError("out_k without K")
-    with _On(dev, stream) as on:
-        keep, args = _rope_args(rope, positions, B, N, dev)
-        outs, ptrs = [], []
-        for x, out, what in ((Q, out_q, "Q"), (K, out_k, "K")):
-            if x is None:
-                outs.append(None)
-                ptrs += [None, None, None, None, 0]
-                continue
-            shape, st = (Q.shape, qs) if x is Q else _heads_tensor(x, what)
-            if (shape[0], shape[2], shape[3]) != (B, N, d) or x.device != dev:
-                raise ValueError("K must match Q in all but its heads")
-            if out is None:
-                out = on.empty(tuple(shape), torch.bfloat16)
-            oshape, ost = _heads_tensor(out, f"out of {what}")
-            if tuple(oshape) != tuple(shape) or out.device != dev:
-                raise ValueError(f"out of {what}: wrong shape or device")
-            outs.append(out)
-            ptrs += [x.data_ptr(), st, out.data_ptr(), ost, shape[1]]
-        rc = lib.fvattn_rope(*ptrs, B, N, d, *args, 1 if inverse else 0, on.stream)
-    _check(rc, "fvattn_rope")
-    return outs[0], outs[1]
+    f = (_native or _native_calls()).rope
+    args = (Q, K, positions, rope, inverse, out_q, out_k)
+    r = f(*args) if stream is None else _on_stream(stream, f, *args)
+    if type(r) is int:
+        _check(r, "fvattn_rope")
+    return r
 
 
 def fvattn_rope_bwd(dQ: torch.Tensor, dK: torch.Tensor | None, positions: torch.Tensor, rope: RopeAxes, *,
@@ -584,23 +522,6 @@ class KvPages(NamedTuple):
     v_exp: torch.Tensor
 
 
-def _pool_args(pages: KvPages, page_table: torch.Tensor, B: int, heads: int, d: int, device):
-    """Checks; returns (block, C arguments from the codes to max_pages)."""
-    k = pages.k_codes
-    if k.dim() != 4 or k.shape[1] != heads or k.shape[3] != d:
-        raise ValueError("pages: expected codes [pages, heads, block, d] matching K")
-    for t in (k, pages.v_codes):
-        if t.dtype != torch.uint8 or t.shape != k.shape or not t.is_contiguous() or t.device != device:
-            raise ValueError("pages: codes are contiguous uint8 tensors of one shape")
-    for t in (pages.k_exp, pages.v_exp):
-        _int32(t, k.shape[:2], "page exponents", device)
-    if page_table.dim() != 2:
-        raise ValueError("page_table: expected int32 [B, max_pages]")
-    _int32(page_table, (B, page_table.shape[1]), "page_table", device)
-    return int(k.shape[2]), (k.data_ptr(), pages.k_exp.data_ptr(), pages.v_codes.data_ptr(), pages.v_exp.data_ptr(),
-                             k.shape[0], page_table.data_ptr(), page_table.shape[1])
-
-
 def fvattn_cache_append(K: torch.Tensor, V: torch.Tensor, pages: KvPages, page_table: torch.Tensor,
                         start: torch.Tensor, *, new_lens: torch.Tensor | None = None,
                         positions: torch.Tensor | None = None, rope: RopeAxes | None = None,
@@ -608,26 +529,12 @@ def fvattn_cache_append(K: torch.Tensor, V: torch.Tensor, pages: KvPages, page_t
     """New keys and values (bf16 [B, heads, T, d], strided as in fvattn_rope) behind the
     start[b] cached tokens of each sequence, the keys turned by ``positions`` and ``rope`` if
     given.  Returns dev_status (FVATTN_ERR_BAD_PAGE: read it after the stream)."""
-    lib = load_library()
-    (B, H, T, d), ks = _heads_tensor(K, "K")
-    vshape, vs = _heads_tensor(V, "V")
-    dev = K.device
-    if vshape != (B, H, T, d) or V.device != dev:
-        raise ValueError("K and V must have one shape")
-    if (positions is None) != (rope is None):
-        raise ValueError("positions and rope belong together")
-    block, pool = _pool_args(pages, page_table, B, H, d, dev)
-    _int32(start, (B,), "start", dev)
-    _int32(new_lens, (B,), "new_lens", dev)
-    with _On(dev, stream) as on:
-        keep, args = (None, (None, 0, None, None, 0, 0, 0)) if rope is None else _rope_args(rope, positions, B, T, dev)
-        if dev_status is None:
-            dev_status = on.empty((1,), torch.int32)
-        _status_word(dev_status, dev)
-        rc = lib.fvattn_cache_append(K.data_ptr(), ks, V.data_ptr(), vs, B, H, T, d, block, *pool, start.data_ptr(),
-                                     _ptr(new_lens), *args, dev_status.data_ptr(), on.stream)
-    _check(rc, "fvattn_cache_append")
-    return dev_status
+    f = (_native or _native_calls()).cache_append
+    args = (K, V, pages, page_table, start, new_lens, positions, rope, dev_status)
+    r = f(*args) if stream is None else _on_stream(stream, f, *args)
+    if type(r) is int:
+        _check(r, "fvattn_cache_append")
+    return r
 
 
 def fvattn_cache_attend_workspace_bytes(B: int, heads: int, group: int, M: int, d: int, block: int,
@@ -642,40 +549,12 @@ def fvattn_cache_attend(Q: torch.Tensor, pages: KvPages, page_table: torch.Tenso
     """Attention of each sequence's newest tokens (Q bf16 [B, heads * group, M, d], strided
     as in fvattn_rope) over its lens[b] cached ones, the new ones among them.  Returns
     (O bf16, LSE fp32, dev_status); rows behind new_lens[b] are left as they were."""
-    lib = load_library()
-    (B, Hq, M, d), qs = _heads_tensor(Q, "Q")
-    dev = Q.device
-    heads = int(pages.k_codes.shape[1]) if pages.k_codes.dim() == 4 else 0
-    if heads < 1 or Hq % heads:
-        raise ValueError("Q has a multiple of the cache's heads")
-    block, pool = _pool_args(pages, page_table, B, heads, d, dev)
-    _int32(lens, (B,), "lens", dev)
-    _int32(new_lens, (B,), "new_lens", dev)
-    group = Hq // heads
-    with _On(dev, stream) as on:
-        if O is None:
-            O = on.empty((B, Hq, M, d), torch.bfloat16)
-        oshape, ost = _heads_tensor(O, "O")
-        if LSE is None:
-            LSE = on.empty((B, Hq, M), torch.float32)
-        if oshape != (B, Hq, M, d) or O.device != dev:
-            raise ValueError("O must match Q")
-        if tuple(LSE.shape) != (B, Hq, M) or LSE.dtype != torch.float32 or not LSE.is_contiguous() or LSE.device != dev:
-            raise ValueError("LSE: expected contiguous fp32 [B, H, M]")
-        if dev_status is None:
-            dev_status = on.empty((1,), torch.int32)
-        _status_word(dev_status, dev)
-        if workspace is None:
-            need = lib.fvattn_cache_attend_workspace_bytes(B, heads, group, M, d, block, pool[-1])
-            workspace = on.empty((max(int(need), 16),), torch.uint8)
-        elif not workspace.is_contiguous() or workspace.device != dev:
-            raise ValueError("workspace: expected a contiguous tensor on Q's device")
-        rc = lib.fvattn_cache_attend(Q.data_ptr(), qs, B, heads, group, M, d, block, *pool, lens.data_ptr(),
-                                     _ptr(new_lens), 1 if causal else 0, O.data_ptr(), ost, LSE.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                     dev_status.data_ptr(), on.stream)
-    _check(rc, "fvattn_cache_attend")
-    return O, LSE, dev_status
+    f = (_native or _native_calls()).cache_attend
+    args = (Q, pages, page_table, lens, new_lens, causal, O, LSE, workspace, dev_status)
+    r = f(*args) if stream is None else _on_stream(stream, f, *args)
+    if type(r) is int:
+        _check(r, "fvattn_cache_attend")
+    return r
 
 
 def check_status(dev_status: torch.Tensor, where: str = "device") -> None:

@@ -1,4 +1,5 @@
-"""Builds libfvattn.so in-tree with nvcc for sm_100a (no JIT cache, no torch extension).
+"""Builds libfvattn.so in-tree with nvcc for sm_100a (no JIT cache, no torch extension), and beside
+it the Python module _binding (host C++ against torch) for the calls that run for single tokens.
 
     python -m top_routed_block_b200._build
 """
@@ -8,10 +9,12 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfvattn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -30,7 +33,35 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _newer(paths, than: str) -> bool:
+    return not os.path.exists(than) or any(os.path.getmtime(p) > os.path.getmtime(than) for p in paths)
+
+
+def _build_binding(force: bool) -> None:
+    src = os.path.join(PKG, "csrc", "binding.cpp")
+    if not force and not _newer([src, os.path.join(ROOT, "include", "fvattn.h")], BINDING):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + ".tmp"
+    subprocess.check_call([
+        "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+        "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+        "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", PKG, "-lfvattn", "-Wl,-rpath,$ORIGIN",
+        "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = _build_library(force, verbose)
+    _build_binding(force)
+    return lib
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and not _stale():
         return LIB
     objdir = os.path.join(PKG, "_build")
