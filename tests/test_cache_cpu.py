@@ -118,7 +118,7 @@ def test_attend_workspace(lib):
     assert ws(2, 3, 4, 9, 128, 128, 5) >= 2 * 2 * 3 * 5 * 128 * 128 * 2
     # few rows: bounded by the grid, not by the cache's length
     assert 0 < ws(1, 8, 1, 1, 128, 128, 1 << 20) < 64 << 20
-    assert ws(1, 1, 1, 1, 64, 64, 1) <= 4096 + 8 * 68 * 4
+    assert 0 < ws(1, 1, 1, 1, 64, 64, 1) < 8 << 20
 
 
 def test_status_of_bad_pages():
@@ -161,26 +161,38 @@ int main() {
     CHECK(checked_page(-1, 4) < 0 && checked_page(4, 4) < 0 && checked_page(3, 4) == 3 && checked_page(0, 4) == 0);
     CHECK(checked_page(-2147483647 - 1, 4) < 0 && checked_page(2147483647, 4) < 0);
     CHECK(clamp_len(-5, 10) == 0 && clamp_len(11, 10) == 10 && clamp_len(10, 10) == 10);
-    // the plan: whole steps, every token once, no more items than the workspace has room for
+    // the plan: the stretches tile the line of units, each unit is found in its own, and a stretch
+    // holds at most two segments that are not whole in it
     std::srand(7);
-    for (int it = 0; it < 20000; ++it) {
-        const int B = 1 + std::rand() % 20, step = 128;
+    for (int it = 0; it < 3000; ++it) {
+        const int B = 1 + std::rand() % 20;
         const long groups = 1 + std::rand() % 90, ctas = 1 + std::rand() % 443;
-        const long cap = 64L * (1 + std::rand() % (it % 3 ? 60 : 20000));
-        std::vector<long> len(B);
-        long tokens = 0, items = 0;
-        for (long &x : len) {
-            x = std::rand() % 4 ? std::rand() % (cap + 1) : 0;
-            tokens += x > 0 ? x : 1;
+        std::vector<long> ends;
+        long total = 0;
+        for (int b = 0; b < B; ++b) {
+            const long len = std::rand() % 4 ? std::rand() % 3000 : 0, u = segment_units(len, 128);
+            CHECK(u >= 1 && u * 128 >= len && (u - 1) * 128 < (len > 0 ? len : 1));
+            for (long k = 0; k < groups; ++k) ends.push_back(total += u);
         }
-        const long chunk = chunk_tokens(tokens, groups, ctas, 4, step);
-        CHECK(chunk >= step && chunk % step == 0);
-        for (long x : len) {
-            const long n = chunks_of(x, chunk);
-            CHECK(n >= 1 && n * chunk >= x && (n - 1) * chunk < (x > 0 ? x : 1));
-            items += n * groups;
+        const long n = stretches(total, ctas);
+        CHECK(n >= 1 && n <= ctas);
+        CHECK(stretch_start(0, total, n) == 0 && stretch_start(n, total, n) == total);
+        for (long c = 0; c < n; ++c) {
+            const long s0 = stretch_start(c, total, n), s1 = stretch_start(c + 1, total, n);
+            CHECK(s0 < s1);
+            for (long u = s0; u < s1; ++u) CHECK(stretch_of(u, total, n) == c);
         }
-        CHECK(items <= max_items(B, groups, cap, ctas, 4, step));
+        long from = 0;
+        std::vector<int> begun(n, 0), carried(n, 0);
+        for (long end : ends) {
+            const int c0 = stretch_of(from, total, n), c1 = stretch_of(end - 1, total, n);
+            if (c0 != c1) {
+                ++begun[c0];
+                for (int c = c0 + 1; c <= c1; ++c) ++carried[c];
+            }
+            from = end;
+        }
+        for (long c = 0; c < n; ++c) CHECK(begun[c] <= 1 && carried[c] <= 1);
     }
     return 0;
 }
@@ -201,25 +213,45 @@ def test_index_arithmetic(tmp_path):
     assert r.returncode == 0, r.stdout
 
 
+def chunk_place(d, row, at):
+    """Where the few-rows kernel keeps byte `at` of a row in shared memory."""
+    byte = row * d + at
+    line = byte >> 7
+    mix = (((line >> 1) & 3) << 1) ^ ((line & 1) << 2) if d == 128 else (line & 3) << 1
+    return (line << 7) + ((((byte >> 4) & 7) ^ mix) << 4) + (byte & 8)
+
+
 @pytest.mark.parametrize("d", [64, 128])
-def test_lanes_cover_each_cached_byte_once(d):
-    """The few-rows kernel's loads of a step of 32 tokens: every byte of the 32 rows by one lane."""
-    for kind in ("k", "v"):
-        hit = np.zeros(32 * d, int)
-        for lane in range(32):
-            g, q = lane >> 2, lane & 3
-            if kind == "k":
-                at = [g * d + q * 16 + (mt * 16 + hf * 8) * d + c * 64 for mt in range(2) for hf in range(2)
-                      for c in range(d // 64)]
-                size = 16
-            else:
-                at = [g * (d // 8) + 2 * q * d + (kg * 16 + (t >> 1) * 8 + (t & 1)) * d for kg in range(2)
-                      for t in range(4)]
-                size = d // 8
-            for a in at:
-                assert a % size == 0
-                hit[a: a + size] += 1
+@pytest.mark.parametrize("step", [32, 64])
+def test_lanes_read_each_cached_byte_once(d, step):
+    """The few-rows kernel: the copies write every place once, the lanes read every byte once in the
+    order of the products, and no two lanes of a quarter (half) warp meet in a bank."""
+    places = sorted(chunk_place(d, r, c) + i for r in range(step) for c in range(0, d, 8) for i in range(8))
+    assert places == list(range(step * d))
+
+    def check(reads, size):
+        hit = np.zeros(step * d, int)
+        for r in reads:   # one instruction: (row, byte) of each lane
+            for lo in range(0, 32, 128 // size):
+                banks = [(chunk_place(d, *x) // 4 + w) % 32 for x in r[lo: lo + 128 // size] for w in range(size // 4)]
+                assert len(set(banks)) == len(banks)
+            for row, at in r:
+                assert at % size == 0
+                hit[row * d + at: row * d + at + size] += 1
         assert (hit == 1).all()
+
+    lanes = [(lane >> 2, lane & 3) for lane in range(32)]
+    check([[(mt * 16 + half * 8 + g, c * 64 + q * 16) for g, q in lanes] for mt in range(step // 16) for half in range(2)
+           for c in range(d // 64)], 16)
+    check([[(kg * 16 + (t >> 1) * 8 + (t & 1) + 2 * q, g * (d // 8)) for g, q in lanes] for kg in range(step // 16)
+           for t in range(4)], d // 8)
+    # the rows in which a lane looks for NaN codes are those it reads
+    for q in range(4):
+        rows, row = [], 2 * q
+        while row < step:
+            rows.append(row)
+            row += 7 if row & 1 else 1
+        assert rows == sorted(kg * 16 + (t >> 1) * 8 + (t & 1) + 2 * q for kg in range(step // 16) for t in range(4))
 
 
 @pytest.mark.parametrize("d,n_pairs", [(64, 32), (128, 64), (128, 32), (64, 8)])

@@ -904,7 +904,7 @@ int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, 
 
 size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block, int max_pages) {
     if (check_attend_shape(B, heads, group, M, d, block, max_pages) != FVATTN_OK) return 0;
-    if (attend_few_rows(group, M)) return attend_few_workspace(B, heads, group, M, d, block, max_pages, kPlanSms);
+    if (attend_few_rows(group, M)) return attend_few_workspace(B, d, kPlanSms);
     return cache_tiles_layout(static_cast<int64_t>(B) * heads, d, block, max_pages).total;
 }
 

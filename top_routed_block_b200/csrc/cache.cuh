@@ -57,7 +57,7 @@ inline int64_t attend_rows(int group, int M) { return static_cast<int64_t>(group
 // Whether the call takes the few-rows kernel (else the pages are expanded and the tensor
 // cores' 128-row tiles run over them).
 bool attend_few_rows(int group, int M);
-size_t attend_few_workspace(int B, int heads, int group, int M, int d, int block, int max_pages, int sms);
+size_t attend_few_workspace(int B, int d, int sms);
 cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream);
 // Pages of every sequence as bf16 K and V [B * heads, cap, d] (zeros from the sequence's end
 // to the next multiple of 128 tokens), and the calls' device checks.  nan_first: int32 [B * heads,

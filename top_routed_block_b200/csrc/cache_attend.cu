@@ -10,28 +10,42 @@
 // s_u + ev, for the products with V, so that the weights 2^(s_u - m + ev - w) <= 1 of pages of
 // very different scales stay in range (w is kept relative to m: beside a large score its
 // low bits would be lost).  They are scaled by 2^15 and rounded to fp16 (relative
-// 2^-11; a weight below 2^-29 of the largest loses bits, below 2^-40 it is zero).  Codes
-// convert to fp16 without loss, and so do the query's values after a power-of-two scale per
-// row that puts its largest in [2^14, 2^15) (bf16 has fewer bits; values 2^-31 below the
-// largest lose bits).  So the products are exact in the tensor cores' fp32 sums.
+// 2^-11; a weight below 2^-29 of the largest loses bits, below 2^-40 it is zero), and the
+// codes of V convert to fp16 without loss.  K takes part as it is, in e4m3: a query's value,
+// scaled per row by a power of two, is the sum of two e4m3 numbers, its first 4 bits and 16 times
+// the next 4 (bf16 has 8; what is left of values below 2^-15 of the row's largest is at most
+// 2^-22 of that).  So the products are exact in the tensor cores' fp32 sums.
 //
-// What bounds it: HBM.  Each cached byte is read once and used for 2 * 8 rows of a matrix
-// instruction; one row or eight cost the same.
+// What bounds it: HBM.  Each cached byte is read once and used for the 8 rows of a matrix
+// instruction; one row or eight cost the same.  More rows take more row tiles of 8, which read
+// the same bytes from L2.  (Tiles of 16 and 24 rows, which convert V once for all of them, have no
+// registers left to hide latency: 20 rows over 4 x 8 heads x 20 k tokens, d 128, took 116 us as one
+// tile of 24 and 83 us as three of 8; 16 rows 62 and 61 us.)
 //
-// Why mma.sync: with 1 to 16 rows a tcgen05 tile (M = 64 or 128) would be almost empty, and
-// its operands would have to be converted from e4m3 to 16 bits through shared memory.  Here
-// the tokens are the M side: S^T = K Q^T and O^T = V^T P^T with m16n8k16, the rows are
-// its N = 8, and the A fragments are the cached bytes themselves, loaded from global
-// memory straight into the lanes that use them (the order of the channels inside a product
-// is free, so each lane takes 16 contiguous bytes) and converted in registers: no shared
-// memory, no barrier, each warp its own tokens.  P^T goes from the accumulators' layout to
-// the B operand's by one 8x8 transpose per 8 tokens.
+// Why mma.sync: with 1 to 8 rows a tcgen05 tile (M = 64 or 128) would be almost empty, and
+// its V would have to be converted from e4m3 to 16 bits through shared memory.  Here the
+// tokens are the M side: S^T = K Q^T with m16n8k32 (e4m3, once for each half of the queries)
+// and O^T = V^T P^T with m16n8k16 (fp16), the rows are N = 8, and the A fragments are the
+// cached bytes in the lanes that use them (the order of the channels inside a product is free,
+// so each lane takes 16 contiguous bytes): each warp its own tokens, no barrier.  P^T
+// goes from the accumulators' layout to the B operand's by one 8x8 transpose per 8 tokens.
 //
-// Split: the cached tokens of a (sequence, key head, row tile) are cut into chunks, planned
-// on the device from the lengths so that the host never waits for them; a persistent grid
-// takes the chunks in turn.  A chunk's four warps take 32 tokens at a time, join in shared
-// memory, and write either the result (one chunk) or a partial, which a second kernel joins
-// in chunk order: no atomics, the same bits every time.
+// Loads: a warp copies its tokens (contiguous in a page) into its own part of shared memory,
+// 512 contiguous bytes an instruction (cp.async), the next step's K once this one's scores are
+// done and its V once this one's products are; loads in flight cost no registers and warps do not
+// wait for each other.  The 16-byte chunks of a 128-byte line are permuted so that both the copies
+// and the lanes' reads in fragment order are free of bank conflicts.  (Copied in fragment
+// order straight from the pages, 64 bytes of 8 rows at a time, reads stop at 5.0 TB/s; in
+// whole lines they reach 6.8: a copy loop alone, 900 MB of pages in random order.)
+//
+// Split: the work is planned on the device from the lengths, so that the host never waits for
+// them.  A segment is one (sequence, key head, row tile), its units 256 tokens.  Much work (8 units
+// for each resident CTA, or more): the line of all segments' units is cut into equal
+// stretches, one a CTA; it does whole segments in passing and leaves partials of the two it
+// shares with its neighbours.  Little work: each segment is cut into its own chunks, as
+// small as the resident CTAs allow, one a CTA, because beginning a segment costs as much as two
+// units.  A second kernel joins partials in order: no atomics, the same bits every time.  Caches of
+// at most 512 tokens take one CTA a segment and one launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
@@ -46,40 +60,41 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 32;               // tokens a warp takes at a time (inside one page: pages hold 64 or 128)
-constexpr int kChunkStep = kStep * kWarps;
-constexpr int kCtasPerSm = 3;
-constexpr int kItemsPerCta = 4;         // chunks a CTA of the grid gets on average
+constexpr int kRows = 8;                // rows of a tile
+constexpr int kStep = 64;               // tokens a warp takes at a time (inside one page: pages hold 64 or 128)
+constexpr int kUnit = kStep * kWarps;   // tokens a CTA takes at a time
+constexpr int kWholeTokens = 512;       // caches this short: a CTA takes a whole segment
+constexpr int kCtasPerSm = 3;           // by shared memory (64 KB each at d 128) and registers
+constexpr int kChunkShare = 8;          // units per CTA below which segments are cut into chunks
+constexpr int kChunkSequences = 64;     // more sequences are not worth the search for the chunk
 constexpr int kJoinThreads = 128;
 constexpr float kWeightLog2 = 15.0f;    // weights are scaled by 2^15 before fp16
+constexpr float kNegInf = -__builtin_huge_valf();
 
-// Work plan, written to the workspace by CTA 0 for the joining kernel (and recomputed by
-// every CTA for itself): prefix[b] = first work item of sequence b.
 struct FewWorkspace {
-    size_t prefix, stats, acc, total;
-    int64_t items;
+    size_t plan, stats, acc, total;
 };
 
-FewWorkspace few_layout(int B, int64_t groups, int rows, int d, int64_t capacity, int ctas) {
+FewWorkspace few_layout(int B, int d, int ctas) {
     FewWorkspace w{};
     Carver c;
-    w.items = max_items(B, groups, capacity, ctas, kItemsPerCta, kChunkStep);
-    w.prefix = c.take<int32_t>(static_cast<size_t>(B) + 1);
-    w.stats = c.take<float>(static_cast<size_t>(w.items) * rows * 4);
-    w.acc = c.take<float>(static_cast<size_t>(w.items) * rows * d);
+    w.plan = c.take<int32_t>(static_cast<size_t>(B) + 2);
+    w.stats = c.take<float4>(static_cast<size_t>(ctas) * 2 * kRows);
+    w.acc = c.take<float>(static_cast<size_t>(ctas) * 2 * kRows * d);
     w.total = align_up(c.off, 256);
     return w;
 }
 
 struct FewArgs {
     AttendLaunch a;
-    int32_t *prefix;
-    float4 *stats;  // [items, tile rows]: m, l, w
-    float *acc;     // [items, tile rows, d]
+    int32_t *plan;    // [B + 2] the plan, from CTA 0 for the joining kernel
+    float4 *stats;    // [2 * ctas, kRows]: m, l, w
+    float *acc;       // [2 * ctas, kRows, d]
     float scale_log2;
     int row_tiles;
-    int work_ctas;
-    bool join;      // whether a sequence may have more than one chunk
+    int ctas;         // that take work
+    bool whole;       // a CTA per segment
+    int log2_block;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -99,10 +114,25 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Two fp32 values -> two e4m3 codes in the low half, nearest, saturating.
+__device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // D (16 x 8) += A (16 x 16) B (16 x 8), fp16 operands, fp32 sums.
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D (16 x 8) += A (16 x 32) B (32 x 8), e4m3 operands, fp32 sums.
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -112,22 +142,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
-
-// The cached bytes: not kept in L1 (this SM reads them once), kept in L2 as usual (another
-// row tile may read them).
-__device__ __forceinline__ uint4 load16(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 load8(const uint8_t *p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
 }
 
 struct Seq {
@@ -180,153 +194,255 @@ __device__ void check_attend(const AttendLaunch &a) {
     if (threadIdx.x == 0) *a.dev_status = any ? FVATTN_ERR_BAD_PAGE : FVATTN_OK;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+// ------------------------------------------------------------------ the plan
 
-// Every CTA makes the same plan from the lengths: the chunk (returned) and the first work
-// item of each sequence (prefix[0..B], shared memory).  One warp, the others wait.
-__device__ int make_plan(const FewArgs &g, int *prefix, int *chunk_s) {
+__device__ __forceinline__ int units_of(int len) { return static_cast<int>(segment_units(len, kUnit)); }
+
+// The plan, in shared memory: first[b] = what comes before sequence b, for b = 0 .. B, in units
+// (stretches) or in chunks of at most first[B + 1] units; first[B + 1] = 0 says stretches.
+// Every CTA makes the same plan in its shared memory: one warp, the others wait.
+__device__ void make_plan(const FewArgs &g, int *first, int *lens) {
     const AttendLaunch &a = g.a;
+    const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
-        const int64_t groups = static_cast<int64_t>(a.pool.heads) * g.row_tiles;
-        int64_t tokens = 0;
+        const int groups = a.pool.heads * g.row_tiles;
+        int total = 0;
         for (int b = lane; b < a.B; b += 32) {
-            const int64_t len = clamp_len(a.lens[b], cap);
-            tokens += len > 0 ? len : 1;
+            lens[b] = static_cast<int>(clamp_len(a.lens[b], cap));
+            total += units_of(lens[b]) * groups;
         }
-        tokens = warp_sum(tokens);
-        int64_t chunk = chunk_tokens(tokens, groups, g.work_ctas, kItemsPerCta, kChunkStep);
-        chunk = chunk < (1 << 30) ? chunk : (1 << 30);
+        total = __reduce_add_sync(0xffffffffu, total);
+        __syncwarp();
+        // the smallest chunk, of 1 .. 32 units, with which every chunk gets its own CTA
+        int chunk = 0;
+        if (total < kChunkShare * g.ctas && a.B <= kChunkSequences) {
+            int n = 0;
+            for (int b = 0; b < a.B; ++b) n += (units_of(lens[b]) + lane) / (lane + 1);
+            const uint32_t fits = __ballot_sync(0xffffffffu, n * groups <= g.ctas);
+            chunk = __ffs(static_cast<int>(fits));  // 0: none
+        }
         int before = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
-            int n = b < a.B ? static_cast<int>(chunks_of(clamp_len(a.lens[b], cap), chunk) * groups) : 0;
+            const int u = b < a.B ? units_of(lens[b]) : 0;
+            const int n = (chunk ? (u + chunk - 1) / chunk : u) * groups;
             int inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += t;
             }
-            if (b < a.B) prefix[b] = before + inc - n;
+            if (b < a.B) first[b] = before + inc - n;
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) {
-            prefix[a.B] = before;
-            *chunk_s = static_cast<int>(chunk);
+            first[a.B] = before;
+            first[a.B + 1] = chunk;
         }
     }
     __syncthreads();
-    return *chunk_s;
 }
 
-// Largest b with prefix[b] <= item.
-__device__ __forceinline__ int find_sequence(const int *prefix, int B, int item) {
+// Largest b with first[b] <= x.
+__device__ __forceinline__ int find_sequence(const int *first, int B, int x) {
     int lo = 0, hi = B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= item) lo = mid;
+        if (first[mid] <= x) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
 
-// A row's sums: l = sum 2^(s - m), acc = 2^15 sum 2^(s - m + ev - w) v.  Without a token m = w =
-// -inf and both are 0.
+// ------------------------------------------------------------------ a row's sums
+
+// l = sum 2^(s - m), acc = 2^15 sum 2^(s - m + ev - w) v.  Without a token m = w = -inf, both are 0.
 __device__ __forceinline__ float out_factor(float l, float w) {
     return l == 0.0f ? 0.0f : ex2(w - kWeightLog2) / l;
 }
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+}
 // m_old - m_new for a maximum that moved from m_old (or -inf) to m_new.
 __device__ __forceinline__ float moved_by(float m_old, float m_new) { return m_old == m_new ? 0.0f : m_old - m_new; }
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+
+// N partial sums of one row as one: their statistics (m, l, w), and the factor of each one's acc.
+struct Joined {
+    float m, w, l;
+    __device__ __forceinline__ Joined() : m(kNegInf), w(kNegInf), l(0.0f) {}
+    __device__ __forceinline__ void top(float m_k) { m = fmaxf(m, m_k); }                        // first all of these,
+    __device__ __forceinline__ void weight(float m_k, float w_k) { w = fmaxf(w, w_k + moved_by(m_k, m)); }  // then these,
+    __device__ __forceinline__ float add(float m_k, float l_k, float w_k) {                      // then these
+        const float shift = moved_by(m_k, m);
+        l += m_k == kNegInf ? l_k : l_k * ex2(shift);  // (without a token 0, or NaN)
+        return w_k == kNegInf ? 1.0f : ex2(w_k + shift - w);
+    }
+};
+
+__device__ __forceinline__ void add_scaled(float4 &sum, const float4 &v, float f) {
+    sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
 }
 
-// Bytes per lane of one V row: 16 at d 128, 8 at d 64.
-template <int D>
-struct VRow;
-template <>
-struct VRow<128> {
-    uint32_t w[4];
-    __device__ __forceinline__ void load(const uint8_t *p) {
-        const uint4 x = load16(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    }
-};
-template <>
-struct VRow<64> {
-    uint32_t w[2];
-    __device__ __forceinline__ void load(const uint8_t *p) {
-        const uint2 x = load8(p);
-        w[0] = x.x, w[1] = x.y;
-    }
-};
+// Four channels of row r (of key head h) from its sums, and the LSE with the first of them.
+__device__ __forceinline__ void write_row(const AttendLaunch &a, int b, int h, int r, int ch, const float4 &sum,
+                                          const Joined &j) {
+    const int64_t hq = h * a.group + r / a.M, tok = r % a.M;
+    const float f = out_factor(j.l, j.w);
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.O) + b * a.o_b + hq * a.o_h + tok * a.o_n + ch;
+    const __nv_bfloat162 p0 = __floats2bfloat162_rn(sum.x * f, sum.y * f);
+    const __nv_bfloat162 p1 = __floats2bfloat162_rn(sum.z * f, sum.w * f);
+    *reinterpret_cast<uint2 *>(out) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&p0), *reinterpret_cast<const uint32_t *>(&p1));
+    if (ch == 0) a.LSE[(static_cast<int64_t>(b) * a.pool.heads * a.group + hq) * a.M + tok] = lse_of(j.m, j.l);
+}
 
-// One warp's 32 tokens of K and V as the lanes use them.
-// K: lane (g = lane / 4, q = lane % 4) has bytes c * 64 + q * 16 .. + 15 (c < D / 64) of tokens
-// mt * 16 + half * 8 + g.  V: bytes g * D/8 .. of tokens kg * 16 + {2q, 2q+1, 2q+8, 2q+9}.
-template <int D>
-struct StepK {
-    uint4 x[2][2][D / 64];
-};
-template <int D>
-struct StepV {
-    VRow<D> x[2][4];
-};
+// ------------------------------------------------------------------ loads
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attend_few_kernel(const __grid_constant__ FewArgs g) {
-    constexpr int ROWS = 8 * NT;
-    constexpr int KS = D / 16;   // k16 steps of K Q^T
-    constexpr int MT = D / 16;   // m16 tiles of V^T P^T
-    constexpr int VW = D / 32;   // words of a lane's V row
-    extern __shared__ int prefix[];
-    __shared__ int chunk_s;
-    __shared__ float4 stat_s[kWarps][ROWS];
-    __shared__ float acc_s[kWarps][8][D];
-    const AttendLaunch &a = g.a;
-    if (blockIdx.x == 0) {
-        make_plan(g, prefix, &chunk_s);
-        if (g.join) {
-            for (int b = threadIdx.x; b <= a.B; b += kThreads) g.prefix[b] = prefix[b];
+// A warp's part of shared memory: a step of K, then one of V, rows in order.  The 16-byte chunks of
+// each 128-byte line (one row at d 128, two at d 64) are permuted by exclusive or with a number
+// that depends on the line.
+template <int D>
+struct Step {
+    static constexpr int BYTES = kStep * D;
+
+    // K's reads take 4 chunks of two neighbouring rows at a time, V's two chunks of every other row
+    // of 8 (d 64: half rows): both hit 8 different chunk places.
+    static __device__ __forceinline__ int mix(int line) {
+        return D == 128 ? (((line >> 1) & 3) << 1) ^ ((line & 1) << 2) : (line & 3) << 1;
+    }
+    // Place of byte `at` (a multiple of 8) of row `row`.
+    static __device__ __forceinline__ int place(int row, int at) {
+        const int byte = row * D + at, line = byte >> 7;
+        return (line << 7) + ((((byte >> 4) & 7) ^ mix(line)) << 4) + (byte & 8);
+    }
+    // One step of K or V from its first byte in the page.
+    static __device__ __forceinline__ void copy(uint32_t dst, const uint8_t *src, int lane) {
+#pragma unroll
+        for (int i = 0; i < BYTES / 512; ++i) {
+            const int line = i * 4 + (lane >> 3);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (line << 7) + (((lane & 7) ^ mix(line)) << 4)),
+                         "l"(src + i * 512 + lane * 16)
+                         : "memory");
         }
+    }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncwarp();  // the other lanes' copies too
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const __grid_constant__ FewArgs g) {
+    constexpr int KW = D / 16;      // words of a lane's part of a query or key row
+    constexpr int MT = D / 16;      // m16 tiles of V^T P^T
+    constexpr int VW = D / 32;      // words of a lane's V row
+    constexpr int ST = kStep / 16;  // 16-token tiles of a step
+    using S_ = Step<D>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    unsigned char *kr = smem + (threadIdx.x >> 5) * 2 * S_::BYTES, *vr = kr + S_::BYTES;  // this warp's K and V
+    float *acc_s = reinterpret_cast<float *>(smem);  // [kWarps][kRows][D], between segments
+    int *first = reinterpret_cast<int *>(smem + kWarps * 2 * S_::BYTES);
+    int *lens = first + g.a.B + 2;
+    __shared__ float4 stat_s[kWarps][kRows];
+    static_assert(kRows * D * 4 <= 2 * S_::BYTES, "the sums reuse the steps' place");
+    const AttendLaunch &a = g.a;
+    const int groups = a.pool.heads * g.row_tiles;
+    if (!g.whole) make_plan(g, first, lens);
+    if (blockIdx.x == 0) {
+        if (!g.whole)
+            for (int i = threadIdx.x; i < a.B + 2; i += kThreads) g.plan[i] = first[i];
         check_attend(a);
         return;
     }
-    const int chunk = make_plan(g, prefix, &chunk_s);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lg = lane >> 2, lq = lane & 3;
     const int BS = a.pool.block, H = a.pool.heads;
     const int R = a.group * a.M;
-    const int n_items = prefix[a.B];
+    const int cta = static_cast<int>(blockIdx.x) - 1;
+    const uint32_t k_at = static_cast<uint32_t>(__cvta_generic_to_shared(kr)), v_at = k_at + S_::BYTES;
 
-    for (int item = static_cast<int>(blockIdx.x) - 1; item < n_items; item += g.work_ctas) {
-        const int b = find_sequence(prefix, a.B, item);
-        const Seq seq = sequence(a, b);
-        const int n_chunks = static_cast<int>(chunks_of(seq.len, chunk));
-        int x = item - prefix[b];
-        const int ci = x % n_chunks;
-        x /= n_chunks;
-        const int rt = x % g.row_tiles;
-        const int h = x / g.row_tiles;
-        const int row0 = rt * ROWS;
-        const int rows = min(ROWS, R - row0);
+    int unit = cta, unit_end = cta + 1, chunk = 0;
+    if (!g.whole) {
+        const int total = first[a.B];
+        chunk = first[a.B + 1];
+        const int n = stretches(total, g.ctas);
+        if (cta >= n) return;
+        if (!chunk) {
+            unit = static_cast<int>(stretch_start(cta, total, n));
+            unit_end = static_cast<int>(stretch_start(cta + 1, total, n));
+        }
+    }
+    while (unit < unit_end) {
+        // the segment, and units [off, off + n_units) of its
+        int b, seg, off = 0, n_units, all;
+        Seq seq;
+        if (g.whole) {
+            b = cta / groups;
+            seg = cta % groups;
+            seq = sequence(a, b);
+            n_units = all = units_of(seq.len);
+            unit = unit_end;
+        } else {
+            b = find_sequence(first, a.B, unit);
+            seq = Seq{lens[b], a.new_lens ? static_cast<int>(clamp_len(__ldg(a.new_lens + b), a.M)) : a.M};
+            all = units_of(seq.len);
+            const int at = unit - first[b];
+            if (chunk) {  // its chunks are as even as can be
+                const int n = (all + chunk - 1) / chunk;
+                seg = at / n;
+                off = static_cast<int>(stretch_start(at % n, all, n));
+                n_units = static_cast<int>(stretch_start(at % n + 1, all, n)) - off;
+                unit = unit_end;
+            } else {
+                seg = at / all;
+                off = at % all;
+                n_units = min(all - off, unit_end - unit);
+                unit += n_units;
+            }
+        }
+        const int h = seg / g.row_tiles, row0 = seg % g.row_tiles * kRows;
+        const int rows = min(kRows, R - row0);
 
-        // query fragments: row nt * 8 + lg, scaled by 2^-sq into fp16
-        uint32_t qf[NT][KS][2];
-        int sq[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = row0 + nt * 8 + lg;
+        const int c1 = seq.n_new == 0 ? 0 : min(seq.len, (off + n_units) * kUnit);
+        const int32_t *table = a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages;
+        // the page and head of the step at `tok`, or -1: behind the end, or an entry outside the pool
+        auto page_at = [&](int tok) -> int64_t {
+            if (tok >= c1) return -1;
+            const int p = checked_page(__ldg(table + (tok >> g.log2_block)), a.pool.num_pages);
+            return p < 0 ? -1 : static_cast<int64_t>(p) * H + h;
+        };
+        // this warp's step at tok is on its way (copy groups K, V); the page of the next is looked up
+        int tok = off * kUnit + warp * kStep;
+        int64_t ph = page_at(tok), ph_next = page_at(tok + kUnit);
+        int ek = 0, ev = 0;
+        {
+            const int64_t at = (ph * BS + (tok & (BS - 1))) * D;
+            if (ph >= 0) {
+                S_::copy(k_at, a.pool.k + at, lane);
+                ek = __ldg(a.pool.ke + ph);
+                ev = __ldg(a.pool.ve + ph);
+            }
+            copies_commit();
+            if (ph >= 0) S_::copy(v_at, a.pool.v + at, lane);
+            copies_commit();
+        }
+
+        // query fragments: row lg, scaled by 2^-sq to at most 448 and split: qh + ql / 16.
+        // Word w of chunk c holds channels c * 64 + lq * 16 + 4 w .. + 3, as K's words do.
+        uint32_t qh[KW], ql[KW];
+        int sq;
+        {
+            const int r = row0 + lg;
             const bool in = r < R && r % a.M < seq.n_new;
             const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(a.Q) + b * a.q_b;
             if (in) qr += static_cast<int64_t>(h * a.group + r / a.M) * a.q_h + static_cast<int64_t>(r % a.M) * a.q_n;
-            float top = 0.0f;
-            uint32_t raw[KS][2];
+            uint32_t raw[KW][2];
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
@@ -339,8 +455,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attend_few
                     raw[c * 4 + w2 * 2 + 1][1] = v.w;
                 }
             }
+            float top = 0.0f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
+            for (int k = 0; k < KW; ++k) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float lo = fabsf(rope_bf16_lo(raw[k][e])), hi = fabsf(rope_bf16_hi(raw[k][e]));
@@ -350,378 +467,315 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attend_few
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            sq[nt] = top > 0.0f ? ilogbf(top) - 14 : 0;
+            sq = top > 0.0f ? ilogbf(top) - 8 : 0;
+            if (scale_pow2(top, -sq) > 448.0f) ++sq;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
+            for (int k = 0; k < KW; ++k) {
+                uint32_t code[2], rest[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    qf[nt][k][e] = f16x2_of(scale_pow2(rope_bf16_lo(raw[k][e]), -sq[nt]),
-                                            scale_pow2(rope_bf16_hi(raw[k][e]), -sq[nt]));
+                for (int e = 0; e < 2; ++e) {
+                    float x0 = scale_pow2(rope_bf16_lo(raw[k][e]), -sq);
+                    float x1 = scale_pow2(rope_bf16_hi(raw[k][e]), -sq);
+                    if (isinf(x0)) x0 = CUDART_NAN_F;  // an infinite query has no softmax either
+                    if (isinf(x1)) x1 = CUDART_NAN_F;
+                    code[e] = codes_of(x0, x1);
+                    const uint32_t y = f16x2_of_codes(code[e]);
+                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+                    rest[e] = codes_of((x0 - z.x) * 16.0f, (x1 - z.y) * 16.0f);
+                }
+                qh[k] = code[0] | (code[1] << 16);
+                ql[k] = rest[0] | (rest[1] << 16);
             }
         }
-        // per lane, rows nt * 8 + 2 lq + e: scale exponent, visible tokens, running statistics
-        int sqr[NT][2];
-        int lim[NT][2];
-        float m[NT][2], w[NT][2], l[NT][2];
+        // per lane, rows 2 lq + e: scale exponent, visible tokens, running statistics
+        int sqr[2], lim[2];
+        float m[2], w[2], l[2];
         int min_lim = seq.len;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int rr = 2 * lq + e, r = row0 + nt * 8 + rr;
-                sqr[nt][e] = __shfl_sync(0xffffffffu, sq[nt], rr * 4);
-                const int tok = r < R ? r % a.M : a.M;
-                lim[nt][e] = r < R ? row_limit(a, seq, tok) : 0;
-                if (r < R && tok < seq.n_new) min_lim = min(min_lim, lim[nt][e]);
-                m[nt][e] = w[nt][e] = -CUDART_INF_F;
-                l[nt][e] = 0.0f;
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int rr = 2 * lq + e, r = row0 + rr;
+            sqr[e] = __shfl_sync(0xffffffffu, sq, rr * 4);
+            const int m_tok = r < R ? r % a.M : a.M;
+            lim[e] = r < R ? row_limit(a, seq, m_tok) : 0;
+            if (r < R && m_tok < seq.n_new) min_lim = min(min_lim, lim[e]);
+            m[e] = w[e] = kNegInf;
+            l[e] = 0.0f;
         }
         min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
         min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
-        float o[NT][MT][4];
+        float o[MT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
+            for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
 
-        // (2^31 tokens: ci * chunk < len + chunk stays below 2^32)
-        const int c0 = static_cast<int>(min(static_cast<int64_t>(ci) * chunk, static_cast<int64_t>(seq.len)));
-        const int c1 = seq.n_new == 0 ? c0 : c0 + min(chunk, seq.len - c0);
-        const int32_t *table = a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages;
-        // the page and head of the step at `tok` (or -1), and its first byte
-        auto page_at = [&](int tok) -> int64_t {
-            if (tok >= c1) return -1;
-            const int p = checked_page(__ldg(table + tok / BS), a.pool.num_pages);
-            return p < 0 ? -1 : static_cast<int64_t>(p) * H + h;
-        };
-        StepK<D> kx;
-        StepV<D> vx;
-        int ek = 0, ev = 0;
-        auto load_k = [&](int64_t ph, int tok) {
-            if (ph < 0) return;
-            const uint8_t *p = a.pool.k + (ph * BS + (tok & (BS - 1))) * D + lg * D + lq * 16;
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c) kx.x[mt][hf][c] = load16(p + (mt * 16 + hf * 8) * D + c * 64);
-        };
-        auto load_v = [&](int64_t ph, int tok) {
-            if (ph < 0) return;
-            const uint8_t *p = a.pool.v + (ph * BS + (tok & (BS - 1))) * D + lg * (D / 8) + 2 * lq * D;
-#pragma unroll
-            for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) vx.x[kg][t].load(p + (kg * 16 + (t >> 1) * 8 + (t & 1)) * D);
-        };
-        int tok = c0 + warp * kStep;
-        int64_t ph = page_at(tok), ph_next = page_at(tok + kChunkStep);
-        load_k(ph, tok);
-        load_v(ph, tok);
-        if (ph >= 0) {
-            ek = __ldg(a.pool.ke + ph);
-            ev = __ldg(a.pool.ve + ph);
-        }
-        for (; tok < c1; tok += kChunkStep) {
-            const int tok_next = tok + kChunkStep;
-            const int64_t ph_after = page_at(tok_next + kChunkStep);
-            int ek_next = 0, ev_next = 0;
-            if (ph_next >= 0) {
-                ek_next = __ldg(a.pool.ke + ph_next);
-                ev_next = __ldg(a.pool.ve + ph_next);
+        for (; tok < c1; tok += kUnit) {
+            const bool here = ph >= 0, more = ph_next >= 0;
+            const int64_t at_next = (ph_next * BS + ((tok + kUnit) & (BS - 1))) * D;
+            const int ek_here = clamp_exp(ek);
+            const float evf = static_cast<float>(clamp_exp(ev));
+            if (more) {
+                ek = __ldg(a.pool.ke + ph_next);
+                ev = __ldg(a.pool.ve + ph_next);
             }
-            if (ph < 0) {  // a page table entry outside the pool: its tokens are left out
-                load_k(ph_next, tok_next);
-                load_v(ph_next, tok_next);
-                ph = ph_next, ph_next = ph_after, ek = ek_next, ev = ev_next;
+            ph = ph_next;
+            ph_next = page_at(tok + 2 * kUnit);
+            copies_wait<1>();  // K of this step
+            if (!here) {       // an entry outside the pool: its tokens are left out
+                copies_wait<0>();
+                if (more) S_::copy(k_at, a.pool.k + at_next, lane);
+                copies_commit();
+                if (more) S_::copy(v_at, a.pool.v + at_next, lane);
+                copies_commit();
                 continue;
             }
-            // S^T = K Q^T
-            float s[NT][2][4];
+            // S^T = K Q^T, the second half of the queries' bits apart
+            float s[ST][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int mt = 0; mt < ST; ++mt) {
+                float lo[4];
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int k = 0; k < 4; ++k) s[mt][k] = lo[k] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s[nt][mt][k] = 0.0f;
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const uint4 &x0 = kx.x[mt][0][k >> 2], &x1 = kx.x[mt][1][k >> 2];
-                    const uint32_t w0 = (k & 3) == 0 ? x0.x : (k & 3) == 1 ? x0.y : (k & 3) == 2 ? x0.z : x0.w;
-                    const uint32_t w1 = (k & 3) == 0 ? x1.x : (k & 3) == 1 ? x1.y : (k & 3) == 2 ? x1.z : x1.w;
-                    const uint32_t a0 = f16x2_of_codes(w0 & 0xffffu), a1 = f16x2_of_codes(w1 & 0xffffu);
-                    const uint32_t a2 = f16x2_of_codes(w0 >> 16), a3 = f16x2_of_codes(w1 >> 16);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(s[nt][mt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+                for (int c = 0; c < D / 64; ++c) {
+                    // rows g and g + 8 of the tile, channels c * 64 + q * 16 .. + 15
+                    const uint4 x0 = *reinterpret_cast<const uint4 *>(kr + S_::place(mt * 16 + lg, c * 64 + lq * 16));
+                    const uint4 x1 = *reinterpret_cast<const uint4 *>(kr + S_::place(mt * 16 + 8 + lg, c * 64 + lq * 16));
+                    mma_e4m3(s[mt], x0.x, x1.x, x0.y, x1.y, qh[c * 4], qh[c * 4 + 1]);
+                    mma_e4m3(lo, x0.x, x1.x, x0.y, x1.y, ql[c * 4], ql[c * 4 + 1]);
+                    mma_e4m3(s[mt], x0.z, x1.z, x0.w, x1.w, qh[c * 4 + 2], qh[c * 4 + 3]);
+                    mma_e4m3(lo, x0.z, x1.z, x0.w, x1.w, ql[c * 4 + 2], ql[c * 4 + 3]);
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[mt][k] = fmaf(lo[k], 0.0625f, s[mt][k]);
             }
-            load_k(ph_next, tok_next);
+            __syncwarp();  // read by all lanes
+            if (more) S_::copy(k_at, a.pool.k + at_next, lane);
+            copies_commit();
             const bool edge = tok + kStep > min_lim;
-            const float evf = static_cast<float>(clamp_exp(ev));
-            // weights for V, transposed into the B operand
-            uint32_t pf[NT][2][2];
-            float alpha[NT][2];
+            // the weights, transposed into the B operand
+            float alpha[2];
             bool moved = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int e = 0; e < 2; ++e) {
+                const float f = scale_pow2(g.scale_log2, clamp_exp(sqr[e] + ek_here));
+                float mx = kNegInf;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = ldexpf(g.scale_log2, sqr[nt][e] + clamp_exp(ek));
-                    float mx = -CUDART_INF_F;
+                for (int mt = 0; mt < ST; ++mt)
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float &v = s[mt][2 * hf + e];
+                        v *= f;
+                        if (edge && tok + mt * 16 + hf * 8 + lg >= lim[e]) v = kNegInf;
+                        mx = fmaxf(mx, v);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float m_new = fmaxf(m[e], mx);
+                const float m_ref = m_new == kNegInf ? 0.0f : m_new;
+                const float shift = moved_by(m[e], m_new);
+                const float w_old = w[e] + shift;
+                const float w_new = fmaxf(w_old, mx - m_ref + evf);
+                const float w_off = w_new == kNegInf ? 0.0f : evf + kWeightLog2 - w_new;
+                const float al = ex2(shift);
+                const bool grew = w_new != w_old && w_old != kNegInf;
+                alpha[e] = grew ? ex2(w_old - w_new) : 1.0f;
+                moved |= grew;
+                float sum = 0.0f;
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            float &v = s[nt][mt][2 * hf + e];
-                            v *= f;
-                            if (edge && tok + mt * 16 + hf * 8 + lg >= lim[nt][e]) v = -CUDART_INF_F;
-                            mx = fmaxf(mx, v);
-                        }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float m_new = fmaxf(m[nt][e], mx);
-                    const float m_ref = m_new == -CUDART_INF_F ? 0.0f : m_new;
-                    const float shift = moved_by(m[nt][e], m_new);
-                    const float w_old = w[nt][e] + shift;
-                    const float w_new = fmaxf(w_old, mx - m_ref + evf);
-                    const float w_off = w_new == -CUDART_INF_F ? 0.0f : evf + kWeightLog2 - w_new;
-                    const float al = ex2(shift);
-                    const bool grew = w_new != w_old && w_old != -CUDART_INF_F;
-                    alpha[nt][e] = grew ? ex2(w_old - w_new) : 1.0f;
-                    moved |= grew;
-                    float sum = 0.0f;
+                for (int mt = 0; mt < ST; ++mt)
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            float &v = s[nt][mt][2 * hf + e];
-                            const float t = v - m_ref;
-                            sum += ex2(t);
-                            v = ex2(t + w_off);
-                        }
-                    l[nt][e] = l[nt][e] * al + sum;
-                    m[nt][e] = m_new;
-                    w[nt][e] = w_new;
-                }
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        pf[nt][mt][hf] = transpose8x8(f16x2_of(s[nt][mt][2 * hf], s[nt][mt][2 * hf + 1]));
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float &v = s[mt][2 * hf + e];
+                        const float t = v - m_ref;
+                        sum += ex2(t);
+                        v = ex2(t + w_off);
+                    }
+                l[e] = l[e] * al + sum;
+                m[e] = m_new;
+                w[e] = w_new;
             }
+            uint32_t pf[ST][2];
+#pragma unroll
+            for (int mt = 0; mt < ST; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) pf[mt][hf] = transpose8x8(f16x2_of(s[mt][2 * hf], s[mt][2 * hf + 1]));
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[nt][i][k] *= alpha[nt][k & 1];
+                    for (int k = 0; k < 4; ++k) o[i][k] *= alpha[k & 1];
             }
+            copies_wait<1>();  // V of this step
             // A step that some row sees only in part (the sequence's end, the causal edge): a
             // NaN among the values of a token that a row does not see must not reach it through
-            // 0 * NaN.  NaN codes become zero, and the rows that do see one get it back below: what
-            // a row sees is a prefix, so the first NaN of a channel decides.
+            // 0 * NaN.  The lane makes its NaN codes zero, and the rows that do see one get it back
+            // here: what a row sees is a prefix, so the first NaN of a channel decides.
             bool nan_here = false;
             if (edge) {
-#pragma unroll
-                for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int k = 0; k < VW; ++k) nan_here |= any_nan_e4m3(vx.x[kg][t].w[k]);
+#pragma unroll 4
+                for (int i = lane; i < S_::BYTES / 16; i += 32) {
+                    const uint4 x = reinterpret_cast<const uint4 *>(vr)[i];
+                    nan_here |= any_nan_e4m3(x.x) || any_nan_e4m3(x.y) || any_nan_e4m3(x.z) || any_nan_e4m3(x.w);
+                }
                 nan_here = __any_sync(0xffffffffu, nan_here);
             }
             if (nan_here) {
-                for (int i = 0; i < MT; ++i) {
-                    for (int half = 0; half < 2; ++half) {
-                        const int byte = 2 * i + half, word = byte >> 2, sh = (byte & 3) * 8;
-                        int first = kStep;
 #pragma unroll
-                        for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                                for (int k = 0; k < VW; ++k)
-                                    if (k == word && ((vx.x[kg][t].w[k] >> sh) & 0x7fu) == 0x7fu) {
-                                        first = min(first, kg * 16 + (t >> 1) * 8 + (t & 1) + 2 * lq);
-                                        vx.x[kg][t].w[k] &= ~(0xffu << sh);
-                                    }
-                        first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
-                        first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                for (int ii = 0; ii < MT; ++ii)
-                                    if (ii == i && first < kStep && tok + first < lim[nt][e]) {
-                                        if (half) o[nt][ii][2 + e] = CUDART_NAN_F;
-                                        else o[nt][ii][e] = CUDART_NAN_F;
-                                    }
+                for (int byte = 0; byte < D / 8; ++byte) {
+                    const int at = lg * (D / 8) + byte;
+                    int seen = kStep;
+#pragma unroll 1
+                    for (int row = 2 * lq; row < kStep; row += (row & 1) ? 7 : 1) {  // this lane's: 2q, 2q + 1 of each 8
+                        unsigned char &code = vr[S_::place(row, at & ~7) + (at & 7)];
+                        if ((code & 0x7fu) != 0x7fu) continue;
+                        code = 0;
+                        seen = min(seen, row);
                     }
+                    seen = min(seen, __shfl_xor_sync(0xffffffffu, seen, 1));
+                    seen = min(seen, __shfl_xor_sync(0xffffffffu, seen, 2));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (seen < kStep && tok + seen < lim[e]) o[byte / 2][(byte & 1) * 2 + e] = CUDART_NAN_F;
                 }
             }
             // O^T += V^T P^T
 #pragma unroll
-            for (int kg = 0; kg < 2; ++kg) {
+            for (int kg = 0; kg < ST; ++kg) {
+                uint32_t vx[4][VW];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {  // tokens 2q, 2q + 1, 2q + 8, 2q + 9 of the 16, channels g * D/8 ..
+                    const unsigned char *x = vr + S_::place(kg * 16 + (t >> 1) * 8 + (t & 1) + 2 * lq, lg * (D / 8));
+                    if constexpr (D == 128) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(x);
+                        vx[t][0] = y.x, vx[t][1] = y.y, vx[t][2] = y.z, vx[t][3] = y.w;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(x);
+                        vx[t][0] = y.x, vx[t][1] = y.y;
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < VW; ++k) {
 #pragma unroll
                     for (int pair = 0; pair < 2; ++pair) {  // bytes 0, 1 and 2, 3 of the word: channels 4k + 2 pair, + 1
                         const uint32_t sel = pair ? 0x7362u : 0x5140u;
-                        const uint32_t x01 = prmt(vx.x[kg][0].w[k], vx.x[kg][1].w[k], sel);
-                        const uint32_t x23 = prmt(vx.x[kg][2].w[k], vx.x[kg][3].w[k], sel);
-                        const uint32_t a0 = f16x2_of_codes(x01 & 0xffffu), a1 = f16x2_of_codes(x01 >> 16);
-                        const uint32_t a2 = f16x2_of_codes(x23 & 0xffffu), a3 = f16x2_of_codes(x23 >> 16);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816(o[nt][2 * k + pair], a0, a1, a2, a3, pf[nt][kg][0], pf[nt][kg][1]);
+                        const uint32_t x01 = __byte_perm(vx[0][k], vx[1][k], sel);
+                        const uint32_t x23 = __byte_perm(vx[2][k], vx[3][k], sel);
+                        mma_f16(o[2 * k + pair], f16x2_of_codes(x01 & 0xffffu), f16x2_of_codes(x01 >> 16),
+                                f16x2_of_codes(x23 & 0xffffu), f16x2_of_codes(x23 >> 16), pf[kg][0], pf[kg][1]);
                     }
                 }
             }
-            load_v(ph_next, tok_next);
-            ph = ph_next, ph_next = ph_after, ek = ek_next, ev = ev_next;
+            __syncwarp();
+            if (more) S_::copy(v_at, a.pool.v + at_next, lane);
+            copies_commit();
         }
+        copies_wait<0>();
+        __syncthreads();  // the steps' place becomes the sums'
 
-        // join the warps: statistics, then eight rows at a time
+        // join the warps
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float sum = l[nt][e];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                if (lg == 0) stat_s[warp][nt * 8 + 2 * lq + e] = make_float4(m[nt][e], sum, w[nt][e], 0.0f);
-            }
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[e];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            if (lg == 0) stat_s[warp][2 * lq + e] = make_float4(m[e], sum, w[e], 0.0f);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (nt * 8 >= rows) break;
+        for (int i = 0; i < MT; ++i) {
+            const int ch = lg * (D / 8) + 2 * i;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int ch = lg * (D / 8) + 2 * i;
-                if (nt * 8 + 2 * lq < rows)
-                    *reinterpret_cast<float2 *>(&acc_s[warp][2 * lq][ch]) = make_float2(o[nt][i][0], o[nt][i][2]);
-                if (nt * 8 + 2 * lq + 1 < rows)
-                    *reinterpret_cast<float2 *>(&acc_s[warp][2 * lq + 1][ch]) = make_float2(o[nt][i][1], o[nt][i][3]);
-            }
-            __syncthreads();
-            for (int y = threadIdx.x; y < min(8, rows - nt * 8) * (D / 4); y += kThreads) {
-                const int rr = y / (D / 4), ch = (y % (D / 4)) * 4;
-                const int r = row0 + nt * 8 + rr;
-                float mm = -CUDART_INF_F, ww = -CUDART_INF_F;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, stat_s[k][nt * 8 + rr].x);
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const float4 st = stat_s[k][nt * 8 + rr];
-                    ww = fmaxf(ww, st.z + moved_by(st.x, mm));
-                }
-                float ll = 0.0f;
-                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const float4 st = stat_s[k][nt * 8 + rr];
-                    const float4 v = *reinterpret_cast<const float4 *>(&acc_s[k][rr][ch]);
-                    const float shift = moved_by(st.x, mm);
-                    // (without a token the sums are 0, or NaN)
-                    ll += st.x == -CUDART_INF_F ? st.y : st.y * ex2(shift);
-                    const float f = st.z == -CUDART_INF_F ? 1.0f : ex2(st.z + shift - ww);
-                    sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
-                }
-                if (n_chunks > 1) {
-                    const int64_t at = static_cast<int64_t>(item) * ROWS + nt * 8 + rr;
-                    if (ch == 0) g.stats[at] = make_float4(mm, ll, ww, 0.0f);
-                    *reinterpret_cast<float4 *>(g.acc + at * D + ch) = sum;
-                } else if (r % a.M < seq.n_new) {
-                    const int64_t hq = h * a.group + r / a.M, tokq = r % a.M;
-                    const float f = out_factor(ll, ww);
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.O) + b * a.o_b + hq * a.o_h + tokq * a.o_n + ch;
-                    const __nv_bfloat162 p0 = __floats2bfloat162_rn(sum.x * f, sum.y * f);
-                    const __nv_bfloat162 p1 = __floats2bfloat162_rn(sum.z * f, sum.w * f);
-                    *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&p0),
-                                                                 *reinterpret_cast<const uint32_t *>(&p1));
-                    if (ch == 0)
-                        a.LSE[(static_cast<int64_t>(b) * H * a.group + hq) * a.M + tokq] = lse_of(mm, ll);
-                }
-            }
-            __syncthreads();
+            for (int e = 0; e < 2; ++e)
+                if (2 * lq + e < rows)
+                    *reinterpret_cast<float2 *>(acc_s + (warp * kRows + 2 * lq + e) * D + ch) = make_float2(o[i][e], o[i][2 + e]);
         }
+        __syncthreads();
+        const bool complete = n_units == all;
+        const int slot = 2 * cta + (off == 0 ? 1 : 0);
+        for (int y = threadIdx.x; y < rows * (D / 4); y += kThreads) {
+            const int rr = y / (D / 4), ch = (y % (D / 4)) * 4;
+            Joined j;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) j.top(stat_s[k][rr].x);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) j.weight(stat_s[k][rr].x, stat_s[k][rr].z);
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 st = stat_s[k][rr];
+                add_scaled(sum, *reinterpret_cast<const float4 *>(acc_s + (k * kRows + rr) * D + ch), j.add(st.x, st.y, st.z));
+            }
+            if (!complete) {
+                const int64_t at = static_cast<int64_t>(slot) * kRows + rr;
+                if (ch == 0) g.stats[at] = make_float4(j.m, j.l, j.w, 0.0f);
+                *reinterpret_cast<float4 *>(g.acc + at * D + ch) = sum;
+            } else if ((row0 + rr) % a.M < seq.n_new) {
+                write_row(a, b, h, row0 + rr, ch, sum, j);
+            }
+        }
+        __syncthreads();
     }
 }
 
-// Joins the chunks of one row: grid (row of the tile's heads, sequence).  The chunks go to the
-// CTA's groups of D / 4 threads in turn and the groups are added in order.
-template <int D, int ROWS>
+// Joins the partials of one row: grid (key head and row, sequence).  They go to the CTA's groups
+// of D / 4 threads in turn, and the groups are added in order.
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ FewArgs g) {
     constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
     __shared__ float4 acc_s[GROUPS][LANES];
     __shared__ float3 stat_s[GROUPS];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the partials are still made
     const AttendLaunch &a = g.a;
     const int b = blockIdx.y;
     const int R = a.group * a.M;
     const int h = blockIdx.x / R, r = blockIdx.x % R;
     const Seq seq = sequence(a, b);
-    const int groups = a.pool.heads * g.row_tiles;
-    const int first_item = g.prefix[b];
-    const int n_chunks = (g.prefix[b + 1] - first_item) / groups;
-    if (n_chunks <= 1 || r % a.M >= seq.n_new) return;
-    const int rt = r / ROWS;
-    const int64_t at0 = (static_cast<int64_t>(first_item) + static_cast<int64_t>(h * g.row_tiles + rt) * n_chunks) * ROWS +
-                        r % ROWS;
+    if (r % a.M >= seq.n_new) return;
+    const int total = g.plan[a.B], before = g.plan[b], chunk = g.plan[a.B + 1], units = units_of(seq.len);
+    const int seg = h * g.row_tiles + r / kRows;
+    // CTAs from..: a segment's first part is the second partial of its CTA (of the segment that CTA
+    // ends in), the others are the first of theirs
+    int from, n_parts;
+    if (chunk) {
+        n_parts = (units + chunk - 1) / chunk;
+        from = before + seg * n_parts;
+    } else {
+        const int n = stretches(total, g.ctas);
+        const int64_t u0 = before + static_cast<int64_t>(seg) * units;
+        from = stretch_of(u0, total, n);
+        n_parts = stretch_of(u0 + units - 1, total, n) - from + 1;
+    }
+    if (n_parts <= 1) return;  // finished where it lies
+    auto part = [&](int c) { return (static_cast<int64_t>(2 * (from + c)) + (c == 0 ? 1 : 0)) * kRows + r % kRows; };
     const int grp = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * 4;
-    float m = -CUDART_INF_F, w = -CUDART_INF_F, l = 0.0f;
-    for (int c = grp; c < n_chunks; c += GROUPS) m = fmaxf(m, g.stats[at0 + static_cast<int64_t>(c) * ROWS].x);
-    for (int c = grp; c < n_chunks; c += GROUPS) {
-        const float4 st = g.stats[at0 + static_cast<int64_t>(c) * ROWS];
-        w = fmaxf(w, st.z + moved_by(st.x, m));
+    Joined j;
+    for (int c = grp; c < n_parts; c += GROUPS) j.top(g.stats[part(c)].x);
+    for (int c = grp; c < n_parts; c += GROUPS) {
+        const float4 st = g.stats[part(c)];
+        j.weight(st.x, st.z);
     }
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = grp; c < n_chunks; c += GROUPS) {
-        const int64_t at = at0 + static_cast<int64_t>(c) * ROWS;
+    for (int c = grp; c < n_parts; c += GROUPS) {
+        const int64_t at = part(c);
         const float4 st = g.stats[at];
-        const float4 v = *reinterpret_cast<const float4 *>(g.acc + at * D + ch);
-        const float shift = moved_by(st.x, m);
-        l += st.x == -CUDART_INF_F ? st.y : st.y * ex2(shift);
-        const float f = st.z == -CUDART_INF_F ? 1.0f : ex2(st.z + shift - w);
-        sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
+        add_scaled(sum, *reinterpret_cast<const float4 *>(g.acc + at * D + ch), j.add(st.x, st.y, st.z));
     }
     acc_s[grp][threadIdx.x % LANES] = sum;
-    if (ch == 0) stat_s[grp] = make_float3(m, l, w);
+    if (ch == 0) stat_s[grp] = make_float3(j.m, j.l, j.w);
     __syncthreads();
     if (grp != 0) return;
-    float mm = -CUDART_INF_F, ww = -CUDART_INF_F;
+    Joined k;
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) mm = fmaxf(mm, stat_s[k].x);
+    for (int i = 0; i < GROUPS; ++i) k.top(stat_s[i].x);
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) ww = fmaxf(ww, stat_s[k].z + moved_by(stat_s[k].x, mm));
-    float ll = 0.0f;
-    float4 all = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < GROUPS; ++i) k.weight(stat_s[i].x, stat_s[i].z);
+    sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) {
-        const float3 st = stat_s[k];
-        const float4 v = acc_s[k][threadIdx.x];
-        const float shift = moved_by(st.x, mm);
-        ll += st.x == -CUDART_INF_F ? st.y : st.y * ex2(shift);
-        const float f = st.z == -CUDART_INF_F ? 1.0f : ex2(st.z + shift - ww);
-        all.x += v.x * f, all.y += v.y * f, all.z += v.z * f, all.w += v.w * f;
-    }
-    const int64_t hq = h * a.group + r / a.M, tokq = r % a.M;
-    const float f = out_factor(ll, ww);
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.O) + b * a.o_b + hq * a.o_h + tokq * a.o_n + ch;
-    const __nv_bfloat162 p0 = __floats2bfloat162_rn(all.x * f, all.y * f);
-    const __nv_bfloat162 p1 = __floats2bfloat162_rn(all.z * f, all.w * f);
-    *reinterpret_cast<uint2 *>(out) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&p0), *reinterpret_cast<const uint32_t *>(&p1));
-    if (ch == 0) a.LSE[(static_cast<int64_t>(b) * a.pool.heads * a.group + hq) * a.M + tokq] = lse_of(mm, ll);
+    for (int i = 0; i < GROUPS; ++i)
+        add_scaled(sum, acc_s[i][threadIdx.x], k.add(stat_s[i].x, stat_s[i].y, stat_s[i].z));
+    write_row(a, b, h, r, ch, sum, k);
 }
 
 // ---------------------------------------------------------------- pages as bf16
@@ -803,53 +857,54 @@ __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __gr
     }
 }
 
-int few_row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
-
-// CTAs that take chunks: the resident ones but for the one that checks.
-int few_work_ctas(int row_tile, int sms) { return sms * (row_tile == 8 ? kCtasPerSm : 2) - 1; }
+// CTAs that take work: the resident ones but for the one that checks.
+int few_ctas(int sms) { return sms * kCtasPerSm - 1; }
 
 }  // namespace
 
 bool attend_few_rows(int group, int M) { return attend_rows(group, M) <= 32; }
 
-size_t attend_few_workspace(int B, int heads, int group, int M, int d, int block, int max_pages, int sms) {
-    const int64_t rows = attend_rows(group, M);
-    const int tile = few_row_tile(rows);
-    return few_layout(B, heads * ceil_div(rows, tile), tile, d, static_cast<int64_t>(max_pages) * block,
-                      few_work_ctas(tile, sms)).total;
-}
+size_t attend_few_workspace(int B, int d, int sms) { return few_layout(B, d, few_ctas(sms)).total; }
 
-template <int D, int NT>
-static cudaError_t launch_few_t(FewArgs &g, int64_t items, cudaStream_t stream) {
+template <int D>
+static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
     const AttendLaunch &a = g.a;
-    const int64_t ctas = items < g.work_ctas ? items : g.work_ctas;
-    const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-    attend_few_kernel<D, NT><<<static_cast<unsigned>(ctas) + 1, kThreads, smem, stream>>>(g);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !g.join) return e;
-    const dim3 grid(static_cast<unsigned>(a.pool.heads * attend_rows(a.group, a.M)), static_cast<unsigned>(a.B));
-    attend_join_kernel<D, 8 * NT><<<grid, kJoinThreads, 0, stream>>>(g);
-    return cudaGetLastError();
+    constexpr size_t steps = static_cast<size_t>(kWarps) * 2 * Step<D>::BYTES;
+    const size_t smem = steps + (2 * static_cast<size_t>(a.B) + 2) * sizeof(int);
+    // (per device and call: the attribute belongs to the device's own copy of the function)
+    cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
+    if (e != cudaSuccess) return e;
+    attend_few_kernel<D><<<static_cast<unsigned>(g.ctas) + 1, kThreads, smem, stream>>>(g);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || g.whole) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.pool.heads * attend_rows(a.group, a.M)), static_cast<unsigned>(a.B));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, g);
 }
 
 cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream) {
-    const int64_t rows = attend_rows(a.group, a.M);
-    const int tile = few_row_tile(rows);
     FewArgs g{};
     g.a = a;
-    g.row_tiles = static_cast<int>(ceil_div(rows, tile));
-    g.work_ctas = few_work_ctas(tile, a.sms);
-    const int64_t capacity = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
-    const FewWorkspace w = few_layout(a.B, static_cast<int64_t>(a.pool.heads) * g.row_tiles, tile, a.pool.d, capacity,
-                                      g.work_ctas);
+    g.row_tiles = static_cast<int>(ceil_div(attend_rows(a.group, a.M), kRows));
+    g.whole = static_cast<int64_t>(a.pool.max_pages) * a.pool.block <= kWholeTokens;
+    const int most = few_ctas(a.sms);
+    const FewWorkspace w = few_layout(a.B, a.pool.d, most);
+    g.ctas = g.whole ? a.B * a.pool.heads * g.row_tiles : most;
+    g.log2_block = a.pool.block == 128 ? 7 : 6;
     char *ws = static_cast<char *>(a.workspace);
-    g.prefix = reinterpret_cast<int32_t *>(ws + w.prefix);
+    g.plan = reinterpret_cast<int32_t *>(ws + w.plan);
     g.stats = reinterpret_cast<float4 *>(ws + w.stats);
     g.acc = reinterpret_cast<float *>(ws + w.acc);
     g.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.pool.d)));
-    g.join = capacity > kChunkStep;
-    if (a.pool.d == 128) return tile == 8 ? launch_few_t<128, 1>(g, w.items, stream) : launch_few_t<128, 2>(g, w.items, stream);
-    return tile == 8 ? launch_few_t<64, 1>(g, w.items, stream) : launch_few_t<64, 2>(g, w.items, stream);
+    return a.pool.d == 128 ? launch_few_t<128>(g, stream) : launch_few_t<64>(g, stream);
 }
 
 cudaError_t launch_cache_expand(const AttendLaunch &a, int64_t cap, void *K, void *V, int32_t *nan_first,

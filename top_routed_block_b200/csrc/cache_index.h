@@ -47,24 +47,16 @@ FVATTN_HD int64_t append_count(int64_t start, int64_t n, int64_t T, int64_t capa
     return n < capacity - start ? n : capacity - start;
 }
 
-// Tokens of one attention work item for `tokens` cached tokens over all sequences (an
-// empty sequence counts one), `groups` (key head, row tile) pairs and `ctas` resident
-// blocks: a multiple of `step`, small enough that a block gets about `per_cta` items.
-FVATTN_HD int64_t chunk_tokens(int64_t tokens, int64_t groups, int64_t ctas, int per_cta, int step) {
-    const int64_t share = (tokens * groups + ctas * per_cta - 1) / (ctas * per_cta);
-    return (share + step - 1) / step * step;
-}
+// Attention of a few rows cuts the line of all segments' units of `unit` tokens into equal
+// stretches.  Units of a segment of `len` cached tokens (an empty one still writes its rows):
+FVATTN_HD int64_t segment_units(int64_t len, int unit) { return len <= 0 ? 1 : (len + unit - 1) / unit; }
 
-// Work items of a sequence of `len` cached tokens (an empty one still writes its rows).
-FVATTN_HD int64_t chunks_of(int64_t len, int64_t chunk) { return len <= 0 ? 1 : (len + chunk - 1) / chunk; }
+// How many stretches for up to `ctas` CTAs: none is empty.
+FVATTN_HD int stretches(int64_t total, int ctas) { return total < ctas ? static_cast<int>(total) : ctas; }
 
-// Upper bound of the work items over all sequences, from sizes the host has: chunk_tokens
-// gives each group at most ctas * per_cta / groups items' worth of tokens and one ragged
-// item per sequence on top, and no chunk is shorter than `step`.
-FVATTN_HD int64_t max_items(int64_t B, int64_t groups, int64_t capacity, int64_t ctas, int per_cta, int step) {
-    const int64_t by_share = ctas * per_cta + B * groups;
-    const int64_t by_step = B * groups * chunks_of(capacity, step);
-    return by_share < by_step ? by_share : by_step;
-}
+// Stretch c of n is [stretch_start(c), stretch_start(c + 1)) of `total` units ...
+FVATTN_HD int64_t stretch_start(int64_t c, int64_t total, int64_t n) { return c * total / n; }
+// ... and unit u lies in stretch
+FVATTN_HD int stretch_of(int64_t u, int64_t total, int64_t n) { return static_cast<int>(((u + 1) * n - 1) / total); }
 
 }  // namespace fvattn
