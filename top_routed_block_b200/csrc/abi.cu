@@ -885,7 +885,9 @@ int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, 
     }
     const int64_t bh = static_cast<int64_t>(B) * heads;
     if (bh >= (1LL << 30) || bh * 2 * max_touched_pages(T, block) + 1 >= (1LL << 31)) return FVATTN_ERR_UNSUPPORTED;
+    DeviceInfo info;
     if ((rc = check_device()) != FVATTN_OK) return rc;
+    if (!device_info(&info)) return FVATTN_ERR_CUDA;
     a.pool = CachePool{k_codes, v_codes, k_exp, v_exp, num_pages, heads, block, d, page_table, max_pages};
     a.K = K;
     a.V = V;
@@ -899,7 +901,7 @@ int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, 
     a.pos_b = pos_batch_stride;
     a.half = pos && pairing == 1;
     a.dev_status = dev_status;
-    return from_cuda(launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_cache_append(a, info.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block, int max_pages) {

@@ -36,7 +36,7 @@ struct AppendLaunch {
     int32_t *dev_status;
 };
 
-cudaError_t launch_cache_append(const AppendLaunch &a, cudaStream_t stream);
+cudaError_t launch_cache_append(const AppendLaunch &a, int sms, cudaStream_t stream);
 
 struct AttendLaunch {
     CachePool pool;
