@@ -226,7 +226,9 @@ int make_rope(RopeParams *p, const double *inv_freq, const int32_t *pair_axis, i
     if (pairing == 1 && n_pairs % 8) return FVATTN_ERR_UNSUPPORTED;
     for (int j = 0; j < n_pairs; ++j) {
         if (!std::isfinite(inv_freq[j]) || pair_axis[j] < 0 || pair_axis[j] >= n_axes) return FVATTN_ERR_INVALID_ARG;
-        p->turns[j] = inv_freq[j] / (2.0 * 3.14159265358979323846);
+        // modulo one revolution, in 2^-64 of it (long double: 64 bits)
+        const long double turns = inv_freq[j] / 6.283185307179586476925286766559L;
+        p->step[j] = static_cast<uint64_t>((turns - std::floor(turns)) * 18446744073709551616.0L);
         p->axis[j] = static_cast<uint8_t>(pair_axis[j]);
     }
     p->n_pairs = n_pairs;

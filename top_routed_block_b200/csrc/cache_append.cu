@@ -16,11 +16,13 @@
 // for single tokens.  One group of threads owns the page of a head while it is appended to, its
 // exponent and its rows: no atomics, nothing written twice.  The values stay in registers
 // between the maximum and the rounding: one read.
-//   Up to 8 tokens: a warp per (sequence, touched page, head, K or V), 4 to a CTA.
-//   More: a CTA of 512 threads per (sequence, touched page, K or V) and group of heads.  The
-//   angles belong to the tokens, so it computes their cosines and sines once, keeps them in
-//   registers and walks its heads, the next head's rows in flight.  (With a CTA per head, each
-//   computing its angles, 4680 tokens of 40 heads, d 128, took 85 us.)
+//   Up to 16 tokens (32 at d 64): a warp per (sequence, touched page, head, K or V), 4 to a CTA.
+//   More: a resident grid of CTAs with 16 channels of a page to a thread.  All (sequence, touched
+//   page, head) form a line of which each takes an equal stretch.  The angles belong to
+//   the tokens, so it computes their cosines and sines once a page, keeps them in registers and
+//   walks the heads, the next head's rows in flight.  (With a CTA per head, each computing its
+//   angles, 4680 tokens of 40 heads, d 128, took 85 us; with as many CTAs as there are groups of
+//   5 heads, which leaves the last wave of them mostly empty, 61.)
 // The CTA behind the last does no work of its own: it checks starts, counts and page table entries
 // and writes the status word, so that the call is one launch.
 #include <cuda_bf16.h>
@@ -35,11 +37,8 @@ namespace fvattn {
 
 namespace {
 
-constexpr int kFewTokens = 8;   // up to here a warp per page
-constexpr int kFewWarps = 4;    // of them in a CTA
-
-// Threads of a CTA that owns a page: two vectors of 8 channels each per pass, at most 512.
-constexpr int append_threads(int d, int block) { return block * d / 16 < 512 ? block * d / 16 : 512; }
+constexpr int kFewWarps = 4;   // warps that own a page each, in a CTA
+constexpr int kFewPasses = 4;  // tokens such a warp takes at most, over those it covers at once
 
 __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
     uint16_t r;
@@ -53,20 +52,42 @@ __device__ __forceinline__ float2 values2(uint32_t two_codes) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// The exponent a largest magnitude asks for (an infinity: 2^0, as the quantizer does).
+// The exponent a largest magnitude (not negative) asks for (an infinity: 2^0, as the quantizer
+// does): from amax = m 2^x with m in [1, 2), x - 8, and one more if m > 448 / 256.
 __device__ __forceinline__ int need_exp(float amax) {
-    if (amax == 0.0f) return kZeroPageExp;
-    if (isinf(amax)) return 0;
-    int e = ilogbf(amax) - 8;  // amax 2^-e in [256, 512)
-    if (scale_pow2(amax, -e) > 448.0f) ++e;
-    return e;
+    const uint32_t bits = __float_as_uint(amax);
+    if (bits >= 0x7f800000u) return 0;
+    if (bits < 0x00800000u) {  // zero or subnormal
+        if (bits == 0) return kZeroPageExp;
+        const int e = ilogbf(amax) - 8;
+        return scale_pow2(amax, -e) > 448.0f ? e + 1 : e;
+    }
+    return static_cast<int>(bits >> 23) - 135 + ((bits & 0x007fffffu) > 0x00600000u ? 1 : 0);
+}
+
+// Largest magnitude of three; NaN is left out.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Sixteen values times 2^-e as codes, two to a half word of q.
+__device__ __forceinline__ void codes16(const float (&v)[16], int e, uint32_t (&q)[8]) {
+    if (e >= -127 && e <= 126) {  // 2^-e is a normal number
+        const float f = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = codes2(v[2 * k] * f, v[2 * k + 1] * f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = codes2(scale_pow2(v[2 * k], -e), scale_pow2(v[2 * k + 1], -e));
+    }
 }
 
 struct AppendArgs {
     AppendLaunch a;
-    int touched;          // pages a sequence's new tokens can touch
-    int heads_per_group;  // heads a group of threads walks
-    int groups;
+    int touched;    // pages a sequence's new tokens can touch
+    int64_t pages;  // (sequence, touched page, head), in this order
 };
 
 __device__ void check_append(const AppendArgs &g) {
@@ -88,55 +109,27 @@ __device__ void check_append(const AppendArgs &g) {
     if (threadIdx.x == 0) *a.dev_status = any ? FVATTN_ERR_BAD_PAGE : FVATTN_OK;
 }
 
-// THREADS threads (a warp, or the whole CTA) own a page; tokens beyond PASSES times what they cover
-// at once do not occur (a page's slots, or kFewTokens).
-template <int D, bool HALF, int THREADS, int PASSES>
-__global__ void __launch_bounds__(THREADS == 32 ? 32 * kFewWarps : THREADS)
-    append_kernel(const __grid_constant__ AppendArgs g) {
-    constexpr int TPT = D / 16;            // threads of a token: two vectors of 8 channels each
-    constexpr int TOKS = THREADS / TPT;    // tokens a pass covers
+// K (TURN) or V of items [item, item_end) by THREADS threads (a warp, or the whole CTA); tokens
+// beyond PASSES times what they cover at once do not occur.
+template <int D, bool HALF, bool FULL, int THREADS, int PASSES, bool TURN>
+__device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, int64_t item_end, const RopeTable &table,
+                                             float (*warp_max)[THREADS / 32], int &barriers) {
+    constexpr int TPT = D / 16;          // threads of a token: two vectors of 8 channels each
+    constexpr int TOKS = THREADS / TPT;  // tokens a pass covers
     constexpr int WARPS = THREADS / 32;
-    __shared__ float warp_max[2][WARPS];   // by turns, so that one barrier a head is enough
+    constexpr bool PREFETCH = true;
     const AppendLaunch &a = g.a;
-    if (blockIdx.x == gridDim.x - 1) {
-        check_append(g);
-        return;
-    }
     const int tid = static_cast<int>(threadIdx.x) % THREADS;
-    int64_t x = THREADS == 32 ? static_cast<int64_t>(blockIdx.x) * kFewWarps + threadIdx.x / 32 : blockIdx.x;
-    const bool is_v = x & 1;
-    x >>= 1;
-    const int h0 = static_cast<int>(x % g.groups) * g.heads_per_group;
-    const int h1 = min(h0 + g.heads_per_group, a.pool.heads);
-    x /= g.groups;
-    const int j = static_cast<int>(x % g.touched);
-    const int64_t b = x / g.touched;
-    if (b >= a.B) return;  // (warps: the last CTA may have more than there are pages)
-
-    const int BS = a.pool.block;
+    const int H = a.pool.heads, BS = a.pool.block;
     const int64_t capacity = static_cast<int64_t>(a.pool.max_pages) * BS;
-    const int64_t start = a.start[b];
-    const int64_t n = append_count(start, a.new_lens ? a.new_lens[b] : a.T, a.T, capacity);
-    if (n <= 0) return;
-    const int64_t pg = start / BS + j;
-    const PageSpan sp = page_span(start, n, pg, BS);
-    if (sp.lo >= sp.hi) return;
-    const int page = checked_page(a.pool.table[b * a.pool.max_pages + pg], a.pool.num_pages);
-    if (page < 0) return;
-
-    uint8_t *codes = (is_v ? a.pool.v : a.pool.k) + static_cast<int64_t>(page) * a.pool.heads * BS * D;
-    int32_t *exps = (is_v ? a.pool.ve : a.pool.ke) + static_cast<int64_t>(page) * a.pool.heads;
-    const __nv_bfloat16 *src = is_v ? static_cast<const __nv_bfloat16 *>(a.V) + b * a.v_b
-                                    : static_cast<const __nv_bfloat16 *>(a.K) + b * a.k_b;
-    const int64_t src_n = is_v ? a.v_n : a.k_n, src_h = is_v ? a.v_h : a.k_h;
-    const bool turn = !is_v && a.pos != nullptr;
-    const bool older = sp.lo > 0;  // slots before the first new token hold older ones
+    const int64_t src_b = TURN ? a.k_b : a.v_b, src_h = TURN ? a.k_h : a.v_h, src_n = TURN ? a.k_n : a.v_n;
 
     // the thread's two vectors: D/2 channels apart, or the two halves of the pairs' channels
     const int i = tid % TPT;
     int ca = 8 * i, cb = 8 * i + D / 2;
     uint32_t on = 0;  // pairs that turn
     int pa = ca / 2, pb = cb / 2;
+    const bool turn = TURN && a.pos != nullptr;
     if (HALF && turn) {
         const int half = a.rope.n_pairs / 8;
         if (i < half) {
@@ -155,138 +148,189 @@ __global__ void __launch_bounds__(THREADS == 32 ? 32 * kFewWarps : THREADS)
             on |= (pb + w < a.rope.n_pairs ? 1u : 0u) << (4 + w);
         }
     }
-    const int slot0 = sp.lo + tid / TPT;  // of pass 0
-    uint4 ra[PASSES], rb[PASSES];
-    auto load = [&](int h) {
+    while (item < item_end) {
+        // heads [h0, h1) of one page
+        const int h0 = static_cast<int>(item % H), h1 = static_cast<int>(min(static_cast<int64_t>(H), h0 + (item_end - item)));
+        const int64_t x = item / H;
+        item += h1 - h0;
+        const int j = static_cast<int>(x % g.touched);
+        const int64_t b = x / g.touched;
+        const int64_t start = a.start[b];
+        const int64_t n = append_count(start, a.new_lens ? a.new_lens[b] : a.T, a.T, capacity);
+        if (n <= 0) continue;
+        const int64_t pg = start / BS + j;
+        const PageSpan sp = page_span(start, n, pg, BS);
+        if (sp.lo >= sp.hi) continue;
+        const int page = checked_page(a.pool.table[b * a.pool.max_pages + pg], a.pool.num_pages);
+        if (page < 0) continue;
+
+        const bool older = sp.lo > 0;         // slots before the first new token hold older ones
+        const int slot0 = sp.lo + tid / TPT;  // of pass 0
+        const int64_t ph = static_cast<int64_t>(page) * H + h0;
+        uint8_t *codes = (TURN ? a.pool.k : a.pool.v) + ph * BS * D;
+        int32_t *exps = (TURN ? a.pool.ke : a.pool.ve) + ph;
+        // the next head's rows, and the exponent its older tokens have
+        const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(TURN ? a.K : a.V) + b * src_b + h0 * src_h +
+                                    (sp.token + tid / TPT) * src_n;
+        uint4 ra[PASSES], rb[PASSES];
+        int e_next = kZeroPageExp;
+        auto load = [&](int ahead) {
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int slot = slot0 + p * TOKS;
-            ra[p] = rb[p] = make_uint4(0, 0, 0, 0);
-            if (slot < sp.hi) {
-                const __nv_bfloat16 *row = src + h * src_h + (sp.token + (slot - sp.lo)) * src_n;
-                ra[p] = __ldg(reinterpret_cast<const uint4 *>(row + ca));
-                rb[p] = __ldg(reinterpret_cast<const uint4 *>(row + cb));
+            for (int p = 0; p < PASSES; ++p) {
+                ra[p] = rb[p] = make_uint4(0, 0, 0, 0);
+                if (slot0 + p * TOKS < sp.hi) {
+                    ra[p] = __ldg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + ca));
+                    rb[p] = __ldg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + cb));
+                }
             }
-        }
-    };
-    load(h0);
-    int e_next = older ? exps[h0] : kZeroPageExp;
-    float c[PASSES][8], s[PASSES][8];
-    if (turn) {
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int slot = slot0 + p * TOKS;
-            if (slot >= sp.hi) continue;
-            const RopePos at = rope_load_pos(a.pos + b * a.pos_b + (sp.token + (slot - sp.lo)) * a.rope.n_axes, a.rope.n_axes);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                c[p][k] = 1.0f;
-                s[p][k] = 0.0f;
-                const int pair = k < 4 ? pa + k : pb + k - 4;
-                if ((on >> k) & 1u) rope_cos_sin(rope_coord(at, a.rope.axis[pair]), a.rope.turns[pair], c[p][k], s[p][k]);
-            }
-        }
-    }
-    for (int h = h0; h < h1; ++h) {
-        const int e_old = clamp_exp(e_next);
-        float v[PASSES][16];
-        float amax = 0.0f;
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const uint32_t w[8] = {ra[p].x, ra[p].y, ra[p].z, ra[p].w, rb[p].x, rb[p].y, rb[p].z, rb[p].w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[p][2 * k] = rope_bf16_lo(w[k]);
-                v[p][2 * k + 1] = rope_bf16_hi(w[k]);
-            }
-        }
-        if (h + 1 < h1) {
-            load(h + 1);
-            e_next = older ? exps[h + 1] : kZeroPageExp;
-        }
+            from += src_h;
+            if (older) e_next = exps[ahead];
+        };
+        load(0);
+        extern __shared__ float4 angles[];  // two pairs' cosines and sines to a float4, the thread's own
+        float4 *mine = angles + threadIdx.x;
+        const int stride = static_cast<int>(blockDim.x);
         if (turn) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                if (slot0 + p * TOKS >= sp.hi) continue;
+                const int slot = slot0 + p * TOKS;
+                if (slot >= sp.hi) continue;
+                const RopePos at =
+                    rope_load_pos(a.pos + b * a.pos_b + (sp.token + (slot - sp.lo)) * a.rope.n_axes, a.rope.n_axes);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    // interleaved: channels 2k, 2k+1 of the 16; half: k and 8 + k
-                    const int m0 = HALF ? k : 2 * k, m1 = HALF ? 8 + k : 2 * k + 1;
-                    const float y0 = v[p][m0], y1 = v[p][m1];
-                    if ((on >> k) & 1u) {
-                        v[p][m0] = fmaf(y0, c[p][k], -y1 * s[p][k]);
-                        v[p][m1] = fmaf(y1, c[p][k], y0 * s[p][k]);
+                for (int w = 0; w < 8; w += 2) {
+                    float4 cs = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+                    const int pair = w < 4 ? pa + w : pb + w - 4;
+                    if ((on >> w) & 1u) rope_cos_sin(rope_coord(at, table.axis[pair]), table.step[pair], cs.x, cs.y);
+                    if ((on >> w) & 2u) rope_cos_sin(rope_coord(at, table.axis[pair + 1]), table.step[pair + 1], cs.z, cs.w);
+                    mine[(p * 4 + w / 2) * stride] = cs;
+                }
+            }
+        }
+        for (int h = h0; h < h1; ++h) {
+            const int e_old = clamp_exp(e_next);
+            float y[PASSES][16];
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const uint32_t w[8] = {ra[p].x, ra[p].y, ra[p].z, ra[p].w, rb[p].x, rb[p].y, rb[p].z, rb[p].w};
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    y[p][2 * q] = rope_bf16_lo(w[q]);
+                    y[p][2 * q + 1] = rope_bf16_hi(w[q]);
+                }
+            }
+            if (PREFETCH && h + 1 < h1) load(1);
+            if (turn) {
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                    if (slot0 + p * TOKS >= sp.hi) continue;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 cs = mine[(p * 4 + q / 2) * stride];
+                        const float c = q & 1 ? cs.z : cs.x, s = q & 1 ? cs.w : cs.y;
+                        // interleaved: channels 2q, 2q+1 of the 16; half: q and 8 + q
+                        const int m0 = HALF ? q : 2 * q, m1 = HALF ? 8 + q : 2 * q + 1;
+                        const float y0 = y[p][m0], y1 = y[p][m1];
+                        if (FULL || ((on >> q) & 1u)) {
+                            y[p][m0] = fmaf(y0, c, -y1 * s);
+                            y[p][m1] = fmaf(y1, c, y0 * s);
+                        }
                     }
                 }
             }
-        }
+            float amax = 0.0f;
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p)
+            for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(v[p][k]));  // fmaxf leaves NaN out
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if constexpr (WARPS > 1) {
-            float *wm = warp_max[(h - h0) & 1];
-            if ((tid & 31) == 0) wm[tid >> 5] = amax;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) amax = fmaxf(amax, wm[w]);
-        }
-        const int e = max(e_old, need_exp(amax));
-        if (tid == 0) exps[h] = e;
-        uint8_t *rows = codes + static_cast<int64_t>(h) * BS * D;
-        if (older && e > e_old) {
-            const int shift = max(e_old - e, -250);
-            uint4 *old = reinterpret_cast<uint4 *>(rows);
-            for (int q = tid; q < sp.lo * (D / 16); q += THREADS) {
-                const uint4 c4 = old[q];
-                uint32_t o4[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x0 = values2(o4[k] & 0xffffu), x1 = values2(o4[k] >> 16);
-                    o4[k] = codes2(scale_pow2(x0.x, shift), scale_pow2(x0.y, shift)) |
-                            (codes2(scale_pow2(x1.x, shift), scale_pow2(x1.y, shift)) << 16);
-                }
-                old[q] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                for (int q = 0; q < 16; q += 2) amax = max_abs(amax, y[p][q], y[p][q + 1]);
+            // (numbers that are not negative order as their bits do)
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            if constexpr (WARPS > 1) {
+                float *wm = warp_max[barriers++ & 1];
+                if ((tid & 31) == 0) wm[tid >> 5] = amax;
+                __syncthreads();
+                const float mine = (tid & 31) < WARPS ? wm[tid & 31] : 0.0f;
+                amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
             }
-        }
+            const int e = max(e_old, need_exp(amax));
+            if (tid == 0) *exps = e;
+            if (older && e > e_old) {
+                const int shift = max(e_old - e, -250);
+                uint4 *old = reinterpret_cast<uint4 *>(codes);
+                for (int q = tid; q < sp.lo * (D / 16); q += THREADS) {
+                    const uint4 c4 = old[q];
+                    uint32_t o4[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int slot = slot0 + p * TOKS;
-            if (slot >= sp.hi) continue;
-            uint32_t q[8];
+                    for (int w = 0; w < 4; ++w) {
+                        const float2 x0 = values2(o4[w] & 0xffffu), x1 = values2(o4[w] >> 16);
+                        o4[w] = codes2(scale_pow2(x0.x, shift), scale_pow2(x0.y, shift)) |
+                                (codes2(scale_pow2(x1.x, shift), scale_pow2(x1.y, shift)) << 16);
+                    }
+                    old[q] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                }
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) q[k] = codes2(scale_pow2(v[p][2 * k], -e), scale_pow2(v[p][2 * k + 1], -e));
-            uint8_t *row = rows + slot * D;
-            *reinterpret_cast<uint2 *>(row + ca) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-            *reinterpret_cast<uint2 *>(row + cb) = make_uint2(q[4] | (q[5] << 16), q[6] | (q[7] << 16));
+            for (int p = 0; p < PASSES; ++p) {
+                const int slot = slot0 + p * TOKS;
+                if (slot >= sp.hi) continue;
+                uint32_t q[8];
+                codes16(y[p], e, q);
+                uint8_t *row = codes + slot * D;
+                *reinterpret_cast<uint2 *>(row + ca) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+                *reinterpret_cast<uint2 *>(row + cb) = make_uint2(q[4] | (q[5] << 16), q[6] | (q[7] << 16));
+            }
+            if (!PREFETCH && h + 1 < h1) load(1);
+            codes += BS * D;
+            ++exps;
         }
     }
 }
 
-template <int D, bool HALF>
-cudaError_t launch_append_t(AppendArgs &g, int sms, cudaStream_t stream) {
-    const AppendLaunch &a = g.a;
-    const int64_t pages = static_cast<int64_t>(a.B) * g.touched * 2;  // K and V apart
-    if (a.T <= kFewTokens) {
-        g.heads_per_group = 1;
-        g.groups = a.pool.heads;
-        const unsigned ctas = static_cast<unsigned>(ceil_div(pages * g.groups, kFewWarps)) + 1;
-        append_kernel<D, HALF, 32, kFewTokens * (D / 16) / 32><<<ctas, 32 * kFewWarps, 0, stream>>>(g);
-        return cudaGetLastError();
+template <int D, bool HALF, bool FULL, int THREADS, int PASSES>
+__global__ void __launch_bounds__(THREADS == 32 ? 32 * kFewWarps : THREADS, THREADS == 32 ? 1 : 1024 / THREADS)
+    append_kernel(const __grid_constant__ AppendArgs g) {
+    __shared__ float warp_max[2][THREADS / 32];  // by turns, so that one barrier a head is enough
+    __shared__ RopeTable table;
+    table.fill(g.a.rope);
+    __syncthreads();
+    if (blockIdx.x == gridDim.x - 1) {
+        check_append(g);
+        return;
     }
-    // heads to a CTA: as many as leave about four CTAs per SM
-    const int64_t per = pages * a.pool.heads / (4LL * sms);
-    g.heads_per_group = static_cast<int>(per < 1 ? 1 : per < a.pool.heads ? per : a.pool.heads);
-    g.groups = static_cast<int>(ceil_div(a.pool.heads, g.heads_per_group));
-    const unsigned ctas = static_cast<unsigned>(pages * g.groups) + 1;
-    if (a.pool.block == 128) {
-        constexpr int T = append_threads(D, 128);
-        append_kernel<D, HALF, T, 128 * (D / 16) / T><<<ctas, T, 0, stream>>>(g);
+    int barriers = 0;
+    if (THREADS == 32) {  // a warp takes K or V of one item
+        const int64_t x = static_cast<int64_t>(blockIdx.x) * kFewWarps + threadIdx.x / 32, item = x >> 1;
+        const int64_t end = min(item + 1, g.pages);
+        if (x & 1) append_items<D, HALF, FULL, THREADS, PASSES, false>(g, item, end, table, warp_max, barriers);
+        else append_items<D, HALF, FULL, THREADS, PASSES, true>(g, item, end, table, warp_max, barriers);
+    } else {  // a CTA takes both of a stretch of them
+        const int64_t item = stretch_start(blockIdx.x, g.pages, gridDim.x - 1);
+        const int64_t end = stretch_start(blockIdx.x + 1, g.pages, gridDim.x - 1);
+        append_items<D, HALF, FULL, THREADS, PASSES, true>(g, item, end, table, warp_max, barriers);
+        append_items<D, HALF, FULL, THREADS, PASSES, false>(g, item, end, table, warp_max, barriers);
+    }
+}
+
+template <int D, bool HALF, bool FULL, int THREADS, int P>
+void launch_append_ctas(const AppendArgs &g, int sms, cudaStream_t stream) {
+    const int64_t resident = static_cast<int64_t>(sms) * (1024 / THREADS) - 1;  // and the one that checks
+    const unsigned ctas = static_cast<unsigned>(g.pages < resident ? g.pages : resident) + 1;
+    cudaFuncSetAttribute(append_kernel<D, HALF, FULL, THREADS, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, P * 64 * THREADS);
+    append_kernel<D, HALF, FULL, THREADS, P><<<ctas, THREADS, P * 64 * THREADS, stream>>>(g);
+}
+
+template <int D, bool HALF, bool FULL>
+cudaError_t launch_append_t(const AppendArgs &g, int sms, cudaStream_t stream) {
+    const AppendLaunch &a = g.a;
+    constexpr int covered = 512 / D;  // tokens of a warp at once
+    if (a.T <= kFewPasses * covered) {
+        const unsigned ctas = static_cast<unsigned>(ceil_div(2 * g.pages, kFewWarps)) + 1;
+        if (a.T <= covered) append_kernel<D, HALF, FULL, 32, 1><<<ctas, 32 * kFewWarps, 64 * 32 * kFewWarps, stream>>>(g);
+        else append_kernel<D, HALF, FULL, 32, kFewPasses><<<ctas, 32 * kFewWarps, kFewPasses * 64 * 32 * kFewWarps, stream>>>(g);
+    } else if (a.pool.block == 128) {
+        launch_append_ctas<D, HALF, FULL, 128 * D / 16, 1>(g, sms, stream);
     } else {
-        constexpr int T = append_threads(D, 64);
-        append_kernel<D, HALF, T, 64 * (D / 16) / T><<<ctas, T, 0, stream>>>(g);
+        launch_append_ctas<D, HALF, FULL, 64 * D / 16, 1>(g, sms, stream);
     }
     return cudaGetLastError();
 }
@@ -294,9 +338,14 @@ cudaError_t launch_append_t(AppendArgs &g, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendLaunch &a, int sms, cudaStream_t stream) {
-    AppendArgs g{a, static_cast<int>(max_touched_pages(a.T, a.pool.block)), 1, 1};
-    if (a.pool.d == 128) return a.half ? launch_append_t<128, true>(g, sms, stream) : launch_append_t<128, false>(g, sms, stream);
-    return a.half ? launch_append_t<64, true>(g, sms, stream) : launch_append_t<64, false>(g, sms, stream);
+    const int64_t touched = max_touched_pages(a.T, a.pool.block);
+    const AppendArgs g{a, static_cast<int>(touched), a.B * touched * a.pool.heads};
+    const bool full = !a.pos || 2 * a.rope.n_pairs == a.pool.d;  // every channel turns
+#define FVATTN_APPEND(D_) \
+    (a.half ? full ? launch_append_t<D_, true, true>(g, sms, stream) : launch_append_t<D_, true, false>(g, sms, stream) \
+            : full ? launch_append_t<D_, false, true>(g, sms, stream) : launch_append_t<D_, false, false>(g, sms, stream))
+    return a.pool.d == 128 ? FVATTN_APPEND(128) : FVATTN_APPEND(64);
+#undef FVATTN_APPEND
 }
 
 }  // namespace fvattn

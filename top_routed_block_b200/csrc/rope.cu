@@ -12,8 +12,7 @@
 // What bounds it: HBM.  Every element is read once and written once (4 bytes of
 // traffic for 3 flop).  The angles belong to a token, not to a head, so a thread
 // keeps the cosines and sines of its 8 channel pairs in registers and walks the
-// heads of both tensors; the fp64 reduction and the sincospif of a pair are paid
-// once per head group.
+// heads of both tensors; a pair's angle is paid for once per head group.
 //
 // Layout of the work: a thread owns two 16-byte vectors (8 channels each) of one
 // token, d/16 threads share a token, and a CTA of 256 threads covers 32 (d 128) or 64
@@ -103,6 +102,9 @@ __global__ void __launch_bounds__(kRopeThreads)
                 const int32_t *__restrict__ pos, int64_t pos_b, int N, int heads_per_group, float sign,
                 const __grid_constant__ RopeParams p) {
     constexpr int TPT = D / 16;  // threads of a token
+    __shared__ RopeTable table;
+    table.fill(p);
+    __syncthreads();
     const int i = threadIdx.x % TPT;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / TPT) + threadIdx.x / TPT;
     if (t >= N) return;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         const int j = w < 4 ? pa + w : pb + w - 4;
         c[w] = 1.0f;
         s[w] = 0.0f;
-        if (FULL || ((on >> w) & 1u)) rope_cos_sin(rope_coord(x, p.axis[j]), p.turns[j], c[w], s[w]);
+        if (FULL || ((on >> w) & 1u)) rope_cos_sin(rope_coord(x, table.axis[j]), table.step[j], c[w], s[w]);
         s[w] *= sign;
     }
     if (h0 < q.heads) walk_heads<HALF, FULL>(q, h0, min(h1, q.heads), b, t, ca, cb, c, s, on);
