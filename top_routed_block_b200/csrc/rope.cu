@@ -32,7 +32,9 @@ namespace fvattn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kHeadsInFlight = 4;  // heads whose loads a thread has outstanding (two 16-byte loads each)
+// Heads whose loads a thread has outstanding (two 16-byte loads each): 8 in long calls, where a
+// thread walks all heads; 2 in short ones, whose few heads to a thread leave more CTAs resident.
+constexpr int kLongAhead = 8, kShortAhead = 2;
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -68,15 +70,15 @@ __device__ __forceinline__ void turn(uint4 &va, uint4 &vb, const float (&c)[8], 
     vb = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-template <bool HALF, bool FULL>
+template <bool HALF, bool FULL, int AHEAD>
 __device__ __forceinline__ void walk_heads(const RopeTensor &x, int h0, int h1, int64_t b, int64_t t, int ca, int cb,
                                            const float (&c)[8], const float (&s)[8], uint32_t on) {
     const __nv_bfloat16 *in = static_cast<const __nv_bfloat16 *>(x.in) + b * x.in_b + t * x.in_n;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(x.out) + b * x.out_b + t * x.out_n;
-    for (int h = h0; h < h1; h += kHeadsInFlight) {
-        uint4 va[kHeadsInFlight], vb[kHeadsInFlight];
+    for (int h = h0; h < h1; h += AHEAD) {
+        uint4 va[AHEAD], vb[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kHeadsInFlight; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             if (h + i < h1) {
                 const __nv_bfloat16 *p = in + (h + i) * x.in_h;
                 va[i] = *reinterpret_cast<const uint4 *>(p + ca);
@@ -84,7 +86,7 @@ __device__ __forceinline__ void walk_heads(const RopeTensor &x, int h0, int h1, 
             }
         }
 #pragma unroll
-        for (int i = 0; i < kHeadsInFlight; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             if (h + i < h1) {
                 turn<HALF, FULL>(va[i], vb[i], c, s, on);
                 __nv_bfloat16 *p = out + (h + i) * x.out_h;
@@ -96,7 +98,7 @@ __device__ __forceinline__ void walk_heads(const RopeTensor &x, int h0, int h1, 
 }
 
 // grid: (token tiles, head groups, B); the heads of q come before those of k.
-template <int D, bool HALF, bool FULL>
+template <int D, bool HALF, bool FULL, int AHEAD>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeTensor q, const __grid_constant__ RopeTensor k,
                 const int32_t *__restrict__ pos, int64_t pos_b, int N, int heads_per_group, float sign,
@@ -144,8 +146,8 @@ __global__ void __launch_bounds__(kRopeThreads)
         if (FULL || ((on >> w) & 1u)) rope_cos_sin(rope_coord(x, table.axis[j]), table.step[j], c[w], s[w]);
         s[w] *= sign;
     }
-    if (h0 < q.heads) walk_heads<HALF, FULL>(q, h0, min(h1, q.heads), b, t, ca, cb, c, s, on);
-    if (h1 > q.heads) walk_heads<HALF, FULL>(k, max(h0 - q.heads, 0), h1 - q.heads, b, t, ca, cb, c, s, on);
+    if (h0 < q.heads) walk_heads<HALF, FULL, AHEAD>(q, h0, min(h1, q.heads), b, t, ca, cb, c, s, on);
+    if (h1 > q.heads) walk_heads<HALF, FULL, AHEAD>(k, max(h0 - q.heads, 0), h1 - q.heads, b, t, ca, cb, c, s, on);
 }
 
 }  // namespace
@@ -155,23 +157,25 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const int32_t 
     const int tokens = kRopeThreads / (d / 16);
     const int64_t tiles = ceil_div(N, tokens);
     const int heads = q.heads + k.heads;
-    // Long inputs: one group, so that a token's angles are computed once.  Short ones are
-    // split over their heads until the grid has about eight CTAs per SM.
-    const int64_t want = ceil_div(8LL * sms, tiles * B);
-    int per_group = static_cast<int>(ceil_div(heads, want < heads ? want : heads));
+    // Two token tiles per SM or more: one group of all heads, so that a token's angles are computed
+    // once.  Fewer: the heads are split until there are about three CTAs per SM.  Measured, us
+    // (40 heads x 32760 tokens d 128; 8 x 32768 d 64; 3 x 7 heads x 1571 d 128): long form 209.3,
+    // 24.9, 11.2; short form 213.7, 26.9, 8.7.
+    const bool is_long = tiles * B >= 2LL * sms;
+    const int64_t groups_wanted = is_long ? 1 : ceil_div(3LL * sms, tiles * B);
+    const int per_group = static_cast<int>(ceil_div(heads, groups_wanted < heads ? groups_wanted : heads));
     const int groups = static_cast<int>(ceil_div(heads, per_group));
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(groups), static_cast<unsigned>(B));
     const bool full = 2 * p.n_pairs == d;
     const float sign = inverse ? -1.0f : 1.0f;
-#define FVATTN_ROPE(D_, H_, F_) \
-    rope_kernel<D_, H_, F_><<<grid, kRopeThreads, 0, stream>>>(q, k, pos, pos_b, N, per_group, sign, p)
-    if (d == 128) {
-        if (half) full ? FVATTN_ROPE(128, true, true) : FVATTN_ROPE(128, true, false);
-        else full ? FVATTN_ROPE(128, false, true) : FVATTN_ROPE(128, false, false);
-    } else {
-        if (half) full ? FVATTN_ROPE(64, true, true) : FVATTN_ROPE(64, true, false);
-        else full ? FVATTN_ROPE(64, false, true) : FVATTN_ROPE(64, false, false);
-    }
+#define FVATTN_ROPE(D_, H_, F_, A_) \
+    rope_kernel<D_, H_, F_, A_><<<grid, kRopeThreads, 0, stream>>>(q, k, pos, pos_b, N, per_group, sign, p)
+#define FVATTN_ROPE_F(D_, H_, A_) (full ? FVATTN_ROPE(D_, H_, true, A_) : FVATTN_ROPE(D_, H_, false, A_))
+#define FVATTN_ROPE_H(D_, A_) (half ? FVATTN_ROPE_F(D_, true, A_) : FVATTN_ROPE_F(D_, false, A_))
+    if (d == 128) is_long ? FVATTN_ROPE_H(128, kLongAhead) : FVATTN_ROPE_H(128, kShortAhead);
+    else is_long ? FVATTN_ROPE_H(64, kLongAhead) : FVATTN_ROPE_H(64, kShortAhead);
+#undef FVATTN_ROPE_H
+#undef FVATTN_ROPE_F
 #undef FVATTN_ROPE
     return cudaGetLastError();
 }
