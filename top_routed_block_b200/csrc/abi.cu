@@ -264,7 +264,7 @@ int check_attend_shape(int B, int heads, int group, int M, int d, int block, int
 }
 
 struct CacheTilesWorkspace {
-    size_t counter, nan_first, zero_bytes, K, V, total;
+    size_t counter, nan_first, zero_bytes, K, V, rest, part_stats, part_acc, total;
     int64_t cap;
 };
 
@@ -277,6 +277,9 @@ CacheTilesWorkspace cache_tiles_layout(int64_t BH, int d, int block, int max_pag
     w.zero_bytes = c.off;
     w.K = c.take<uint16_t>(static_cast<size_t>(BH) * w.cap * d);
     w.V = c.take<uint16_t>(static_cast<size_t>(BH) * w.cap * d);
+    w.rest = c.take<int32_t>(kPlanSms + 1);
+    w.part_stats = c.take<float2>(static_cast<size_t>(kPlanSms) * 2 * 128);
+    w.part_acc = c.take<float>(static_cast<size_t>(kPlanSms) * 2 * 128 * d);
     w.total = align_up(c.off, 256);
     return w;
 }
@@ -312,7 +315,13 @@ int attend_tiles(const AttendLaunch &a, cudaStream_t s) {
     l.Q = a.Q;
     l.tmap_k = &mk;
     l.tmap_v = &mv;
-    l.n_items = static_cast<int>(BH * ct.row_tiles);
+    const int64_t items = BH * ct.row_tiles;
+    const int grid = a.sms;  // CTAs of the attention kernel: one an SM
+    ct.n_rest = static_cast<int>(items % grid);
+    ct.rest = reinterpret_cast<int32_t *>(ws + w.rest);
+    ct.part_stats = reinterpret_cast<float2 *>(ws + w.part_stats);
+    ct.part_acc = reinterpret_cast<float *>(ws + w.part_acc);
+    l.n_items = static_cast<int>(items - ct.n_rest);
     l.work_counter = reinterpret_cast<int *>(ws + w.counter);
     l.N = static_cast<int>(w.cap);
     l.nb = static_cast<int>(w.cap / 128);
@@ -952,9 +961,7 @@ int fvattn_cache_attend(const void *Q, const int64_t *q_strides, int B, int head
     a.workspace = workspace;
     a.sms = info.sms < kPlanSms ? info.sms : kPlanSms;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (attend_few_rows(group, M)) return from_cuda(launch_attend_few(a, s));
-    a.sms = info.sms;
-    return attend_tiles(a, s);
+    return attend_few_rows(group, M) ? from_cuda(launch_attend_few(a, s)) : attend_tiles(a, s);
 }
 
 }  // extern "C"

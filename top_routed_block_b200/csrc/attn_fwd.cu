@@ -206,6 +206,44 @@ __device__ __forceinline__ int cache_tiles_of(const CacheTiles &ct, int item) {
     return static_cast<int>((sees + kKT - 1) / kKT);
 }
 
+// The items behind the whole ones (CacheTiles), cut into equal stretches of their key tiles.
+struct CacheRest {
+    int64_t at, end;  // this CTA's stretch
+    int n_whole;
+
+    __device__ __forceinline__ void open(const CacheTiles &ct, int whole, int cta, int ctas) {
+        n_whole = whole;
+        const int64_t total = ct.rest[ct.n_rest];
+        const int n = stretches(total, ctas);
+        at = cta < n ? stretch_start(cta, total, n) : 0;
+        end = cta < n ? stretch_start(cta + 1, total, n) : 0;
+    }
+    // The next piece: {item, first key tile << 1 | whether others have the rest of it, key tiles, -}.
+    __device__ __forceinline__ bool next(const CacheTiles &ct, int4 &piece) {
+        if (at >= end) return false;
+        int lo = 0, hi = ct.n_rest - 1;
+        while (lo < hi) {  // the last item that begins at or before `at`
+            const int mid = (lo + hi + 1) >> 1;
+            if (__ldg(ct.rest + mid) <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        const int begin = __ldg(ct.rest + lo), units = __ldg(ct.rest + lo + 1) - begin;
+        const int off = static_cast<int>(at) - begin;
+        const int n = static_cast<int>(min(static_cast<int64_t>(units - off), end - at));
+        at += n;
+        // (an item without key tiles has one unit, so that its rows are written)
+        const int tiles = max(min(cache_tiles_of(ct, n_whole + lo) - off, n), 0);
+        piece = make_int4(n_whole + lo, off << 1 | (n < units ? 1 : 0), tiles, n_whole + lo + 1);
+        return true;
+    }
+};
+
+// A row of a piece whose item others share: its sums to the partials' place.  Slot 2 cta + 1: of the
+// item that the CTA's stretch ends in; 2 cta: of the one it begins in.
+__device__ __forceinline__ int64_t cache_part_row(bool begins, int cta, int r) {
+    return (static_cast<int64_t>(2 * cta) + (begins ? 1 : 0)) * kRowsM + r;
+}
+
 // ------------------------------------------------------------- block-64 pairs
 // Pair i of head bh: query blocks 2i (row A) and 2i+1 (row B, absent when nb is
 // odd and i is the last pair).  The 32 lanes of a warp set one bit per selected
@@ -412,12 +450,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             prefetch_tensormap(&tmap_v);
             uint32_t it = 0, rc = 0;  // items published, ring loads issued
             bool ok = true;
+            CacheRest rest{0, 0, -1};  // opened once the queue of whole items is empty
             while (ok) {
-                const int idx = atomicAdd(work_counter, 1);
-                const int rw = (idx < n_items) ? (CACHE ? idx : order[idx]) : -1;
+                const int idx = !CACHE || rest.n_whole < 0 ? atomicAdd(work_counter, 1) : n_items;
+                int rw = (idx < n_items) ? (CACHE ? idx : order[idx]) : -1;
                 int4 item = make_int4(-1, 0, 0, 0);
-                if (CACHE && rw >= 0) {
-                    item = make_int4(rw, 0, cache_tiles_of(ct, rw), idx + 1);
+                if (CACHE) {
+                    if (rw >= 0) {
+                        item = make_int4(rw, 0, cache_tiles_of(ct, rw), idx + 1);
+                    } else {
+                        if (rest.n_whole < 0) rest.open(ct, n_items, blockIdx.x, gridDim.x);
+                        if (rest.next(ct, item)) rw = item.x;
+                    }
                 } else if (rw >= 0) {
                     int c = row_ptr[rw + 1] - row_ptr[rw];
                     if (c < 0) {
@@ -436,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 int prev = -1;
                 int kblk_next = !CACHE && item.z > 0 ? __ldg(col_idx + item.y) : 0;  // loaded one tile ahead
                 for (int j = 0; j < item.z && ok; ++j) {
-                    int kblk = CACHE ? j : kblk_next;
+                    int kblk = CACHE ? (item.y >> 1) + j : kblk_next;
                     if (!CACHE && j + 1 < item.z) kblk_next = __ldg(col_idx + item.y + j + 1);
                     if (CACHE || (kblk >= 0 && kblk < nb && kblk > prev)) {
                         prev = kblk;
@@ -647,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             mine[h] = e >= 0 && ((e >> half) & 1);
                         }
                     } else if constexpr (CACHE) {
-                        kb[0] = j;
+                        kb[0] = (start >> 1) + j;  // start: first key tile << 1 | partial
                         mine[0] = true;
                     } else {
                         kb[0] = kblk_next;
@@ -839,6 +883,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 ++on;
                 tc_fence_after();
                 const bool row_ok = CACHE ? crow.valid : t_row < N;
+                const bool partial = CACHE && (start & 1);
+                float *part = nullptr;
+                if (CACHE && partial) {
+                    const int64_t at = cache_part_row((start >> 1) == 0, blockIdx.x, r);
+                    part = ct.part_acc + at * D;
+                    ct.part_stats[at] = make_float2(m, l);
+                }
                 const float inv_l = (CACHE ? l != 0.0f : l > 0.0f) ? (F8 ? pow2_scale(1.0f / l, e_ref) : 1.0f / l) : 0.0f;
                 __nv_bfloat16 *orow = O + (CACHE ? crow.o_at : (bh * N + t_row) * D);
                 const uint32_t tO = tmem + lane_base + C::T_O;
@@ -851,6 +902,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     } else {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) o[c] = 0u;
+                    }
+                    if (CACHE && partial) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<uint4 *>(part + c0 + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        continue;
                     }
                     uint32_t pkk[16];
 #pragma unroll
@@ -876,7 +933,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             dst[q] = make_uint4(pkk[4 * q], pkk[4 * q + 1], pkk[4 * q + 2], pkk[4 * q + 3]);
                     }
                 }
-                if (row_ok && CACHE)  // a NaN sum stays one
+                if (row_ok && CACHE && partial) {
+                } else if (row_ok && CACHE)  // a NaN sum stays one
                     LSE[crow.lse_at] = (l == 0.0f) ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
                 else if (row_ok)
                     LSE[bh * N + t_row] = (l > 0.0f) ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
@@ -896,6 +954,70 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         cta_busy_ns[blockIdx.x] = t_end - bar->t_start;
     }
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// The plan of the items behind the whole ones: rest[i] = key tiles (at least one each) of the first i
+// of them.  One CTA.
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) cache_rest_kernel(const __grid_constant__ CacheTiles ct, int n_whole) {
+    __shared__ int sums[kPlanThreads];
+    int before = 0;
+    for (int i0 = 0; i0 < ct.n_rest; i0 += kPlanThreads) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        const int n = i < ct.n_rest ? max(cache_tiles_of(ct, n_whole + i), 1) : 0;
+        sums[threadIdx.x] = n;
+        __syncthreads();
+        for (int o = 1; o < kPlanThreads; o <<= 1) {
+            const int t = static_cast<int>(threadIdx.x) >= o ? sums[threadIdx.x - o] : 0;
+            __syncthreads();
+            sums[threadIdx.x] += t;
+            __syncthreads();
+        }
+        if (i < ct.n_rest) ct.rest[i] = before + sums[threadIdx.x] - n;
+        before += sums[kPlanThreads - 1];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) ct.rest[ct.n_rest] = before;
+}
+
+// Joins the partials of the rest items' rows, in the order of their stretches: grid (4 rows, item),
+// a warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheTiles ct, int n_whole, int ctas,
+                                                         __nv_bfloat16 *__restrict__ O, float *__restrict__ LSE) {
+    constexpr int E = D / 32;  // channels of a lane
+    const int i = blockIdx.y, r = blockIdx.x * 4 + (static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    const int64_t total = ct.rest[ct.n_rest], u0 = ct.rest[i], u1 = ct.rest[i + 1];
+    const int n = stretches(total, ctas);
+    const int from = stretch_of(u0, total, n), parts = stretch_of(u1 - 1, total, n) - from + 1;
+    if (parts <= 1) return;  // finished where it lies
+    const CacheRow crow = cache_row(ct, n_whole + i, r);
+    if (!crow.valid) return;
+    auto at = [&](int p) { return cache_part_row(p == 0, from + p, r); };
+    float m = -CUDART_INF_F;
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, ct.part_stats[at(p)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f, acc[E] = {};
+    for (int p = 0; p < parts; ++p) {
+        const float2 st = ct.part_stats[at(p)];
+        const float f = st.x == m ? 1.0f : ex2_approx(st.x - m);  // (a part that sees no token: -inf, and sums 0)
+        l += st.y * f;
+        const float *a = ct.part_acc + at(p) * D + lane * E;
+#pragma unroll
+        for (int c = 0; c < E; ++c) acc[c] += a[c] * f;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t bh = (n_whole + i) / ct.row_tiles;
+#pragma unroll
+    for (int c = 0; c < E; c += 2) {
+        uint32_t w = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+        const int2 f = *reinterpret_cast<const int2 *>(ct.nan_first + bh * D + lane * E + c);
+        if (f.x > 0x7fffffff - crow.limit) w |= 0x7fffu;  // the row sees a NaN value there
+        if (f.y > 0x7fffffff - crow.limit) w |= 0x7fff0000u;
+        *reinterpret_cast<uint32_t *>(O + crow.o_at + lane * E + c) = w;
+    }
+    if (lane == 0) LSE[crow.lse_at] = l == 0.0f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
 // Block 64: the key-block union size of every pair (one warp per pair), the work
@@ -1070,7 +1192,7 @@ static cudaError_t launch_t(const AttnLaunch &a, cudaStream_t stream, const Cach
     }
     if (per_sm < 0) return cudaErrorInvalidConfiguration;
     const int64_t cap = static_cast<int64_t>(per_sm) * a.sms;
-    const int grid = static_cast<int>(a.n_items < cap ? a.n_items : cap);
+    const int grid = static_cast<int>(!CACHE && a.n_items < cap ? a.n_items : cap);
     if (a.grid_out) *a.grid_out = grid;
     if (grid <= 0) return cudaSuccess;
     kern<<<grid, kThreads, Cfg<D, BS, F8>::SMEM_BYTES, stream>>>(
@@ -1093,8 +1215,14 @@ cudaError_t launch_sparse_attn_fp8(const AttnLaunch &a, int bs, cudaStream_t str
 }
 
 cudaError_t launch_cache_tiles(const AttnLaunch &a, const CacheTiles &ct, int d, cudaStream_t stream) {
-    if (d == 128) return launch_t<128, 128, false, true>(a, stream, ct);
-    return launch_t<64, 128, false, true>(a, stream, ct);
+    if (ct.n_rest > 0) cache_rest_kernel<<<1, kPlanThreads, 0, stream>>>(ct, a.n_items);
+    cudaError_t e = d == 128 ? launch_t<128, 128, false, true>(a, stream, ct) : launch_t<64, 128, false, true>(a, stream, ct);
+    if (e != cudaSuccess || ct.n_rest == 0) return e;
+    const dim3 grid(kRowsM / 4, static_cast<unsigned>(ct.n_rest));
+    __nv_bfloat16 *O = static_cast<__nv_bfloat16 *>(a.O);
+    if (d == 128) cache_join_kernel<128><<<grid, 128, 0, stream>>>(ct, a.n_items, a.sms * kCtasPerSm, O, a.LSE);
+    else cache_join_kernel<64><<<grid, 128, 0, stream>>>(ct, a.n_items, a.sms * kCtasPerSm, O, a.LSE);
+    return cudaGetLastError();
 }
 
 }  // namespace fvattn
