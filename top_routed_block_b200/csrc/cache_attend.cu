@@ -795,20 +795,24 @@ struct ExpandArgs {
     int pages;
 };
 
-__device__ __forceinline__ uint4 expand8(uint32_t lo, uint32_t hi, int e) {
+// Eight codes times 2^e (f, where that is a normal number).
+__device__ __forceinline__ uint4 expand8(uint2 codes, int e, bool plain, float f) {
     uint32_t out[4];
-    const uint32_t c[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+    const uint32_t c[4] = {codes.x & 0xffffu, codes.x >> 16, codes.y & 0xffffu, codes.y >> 16};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t h = f16x2_of_codes(c[i]);
-        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        const __nv_bfloat162 y = __floats2bfloat162_rn(scale_pow2(v.x, e), scale_pow2(v.y, e));
+        float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        v = plain ? make_float2(v.x * f, v.y * f) : make_float2(scale_pow2(v.x, e), scale_pow2(v.y, e));
+        const __nv_bfloat162 y = __floats2bfloat162_rn(v.x, v.y);
         out[i] = *reinterpret_cast<const uint32_t *>(&y);
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+template <int D>
 __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __grid_constant__ ExpandArgs g) {
+    constexpr int PER_ROW = D / 8, AHEAD = 64 * PER_ROW / kExpandThreads;  // a vector: 8 codes; 64 rows at a time
     const AttendLaunch &a = g.a;
     if (blockIdx.x == 0) {
         check_attend(a);
@@ -819,41 +823,45 @@ __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __gr
     x /= g.pages;
     const int h = static_cast<int>(x % a.pool.heads);
     const int b = static_cast<int>(x / a.pool.heads);
-    const int BS = a.pool.block, D = a.pool.d;
-    const int64_t len = sequence(a, b).len;
-    const int64_t tok0 = static_cast<int64_t>(pg) * BS;
-    if (tok0 >= static_cast<int64_t>(align_up(static_cast<size_t>(len), 128))) return;
-    const int fill = static_cast<int>(clamp_len(len - tok0, BS));  // cached slots of the page
-    const int page = fill > 0 ? checked_page(a.pool.table[static_cast<int64_t>(b) * a.pool.max_pages + pg], a.pool.num_pages) : -1;
+    const int BS = a.pool.block;
+    const Seq seq = sequence(a, b);
+    const int tok0 = pg * BS;
+    if (seq.n_new == 0 || tok0 >= static_cast<int>(align_up(static_cast<size_t>(seq.len), 128))) return;
+    const int fill = max(min(seq.len - tok0, BS), 0);  // cached slots of the page
+    const int page =
+        fill > 0 ? checked_page(a.pool.table[static_cast<int64_t>(b) * a.pool.max_pages + pg], a.pool.num_pages) : -1;
     const int64_t ph = static_cast<int64_t>(page < 0 ? 0 : page) * a.pool.heads + h;
     const int64_t bh = static_cast<int64_t>(b) * a.pool.heads + h;
-    const int ek = page < 0 ? 0 : clamp_exp(a.pool.ke[ph]), ev = page < 0 ? 0 : clamp_exp(a.pool.ve[ph]);
-    const uint2 *kc = reinterpret_cast<const uint2 *>(a.pool.k + ph * BS * D);
-    const uint2 *vc = reinterpret_cast<const uint2 *>(a.pool.v + ph * BS * D);
-    uint4 *ko = reinterpret_cast<uint4 *>(g.K + (bh * g.cap + tok0) * D);
-    uint4 *vo = reinterpret_cast<uint4 *>(g.V + (bh * g.cap + tok0) * D);
-    const int per_row = D / 8;
-    for (int i = threadIdx.x; i < BS * per_row; i += kExpandThreads) {
-        const int slot = i / per_row;
-        if (page < 0 || slot >= fill) {
-            ko[i] = vo[i] = make_uint4(0, 0, 0, 0);
-            continue;
+    const int rows = page < 0 ? 0 : fill;
+#pragma unroll 1
+    for (int part = 0; part < BS / 32; ++part) {  // K, then V, 64 rows at a time
+        const bool is_v = part >= BS / 64;
+        const int row0 = (is_v ? part - BS / 64 : part) * 64;
+        const int e = page < 0 ? 0 : clamp_exp((is_v ? a.pool.ve : a.pool.ke)[ph]);
+        const bool plain = e >= -126 && e <= 127;
+        const float f = plain ? __int_as_float((e + 127) << 23) : 0.0f;
+        const uint2 *src = reinterpret_cast<const uint2 *>((is_v ? a.pool.v : a.pool.k) + (ph * BS + row0) * D);
+        uint4 *dst = reinterpret_cast<uint4 *>((is_v ? g.V : g.K) + (bh * g.cap + tok0 + row0) * D);
+        uint2 c[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = i * kExpandThreads + threadIdx.x;
+            c[i] = row0 + at / PER_ROW < rows ? __ldcs(src + at) : make_uint2(0, 0);
         }
-        const uint2 kk = __ldcs(kc + i);
-        uint2 vv = __ldcs(vc + i);
-        ko[i] = expand8(kk.x, kk.y, ek);
-        if (any_nan_e4m3(vv.x) || any_nan_e4m3(vv.y)) {
-            for (int y = 0; y < 8; ++y) {
-                uint32_t &word = y < 4 ? vv.x : vv.y;
-                const int sh = (y & 3) * 8;
-                if (((word >> sh) & 0x7fu) == 0x7fu) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = i * kExpandThreads + threadIdx.x;
+            if (is_v && (any_nan_e4m3(c[i].x) || any_nan_e4m3(c[i].y))) {
+                for (int y = 0; y < 8; ++y) {
+                    uint32_t &word = y < 4 ? c[i].x : c[i].y;
+                    const int sh = (y & 3) * 8;
+                    if (((word >> sh) & 0x7fu) != 0x7fu) continue;
                     word &= ~(0xffu << sh);
-                    atomicMax(g.nan_first + bh * D + (i % per_row) * 8 + y,
-                              0x7fffffff - static_cast<int>(tok0 + slot));
+                    atomicMax(g.nan_first + bh * D + at % PER_ROW * 8 + y, 0x7fffffff - (tok0 + row0 + at / PER_ROW));
                 }
             }
+            dst[at] = expand8(c[i], e, plain, f);
         }
-        vo[i] = expand8(vv.x, vv.y, ev);
     }
 }
 
@@ -912,7 +920,8 @@ cudaError_t launch_cache_expand(const AttendLaunch &a, int64_t cap, void *K, voi
     ExpandArgs g{a, cap, static_cast<__nv_bfloat16 *>(K), static_cast<__nv_bfloat16 *>(V), nan_first,
                  static_cast<int>(cap / a.pool.block)};
     const int64_t ctas = static_cast<int64_t>(a.B) * a.pool.heads * g.pages + 1;
-    cache_expand_kernel<<<static_cast<unsigned>(ctas), kExpandThreads, 0, stream>>>(g);
+    if (a.pool.d == 128) cache_expand_kernel<128><<<static_cast<unsigned>(ctas), kExpandThreads, 0, stream>>>(g);
+    else cache_expand_kernel<64><<<static_cast<unsigned>(ctas), kExpandThreads, 0, stream>>>(g);
     return cudaGetLastError();
 }
 
