@@ -13,7 +13,7 @@
 #include "fvattn.h"
 #include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
-#include "cache.cuh"
+#include "cache_tiles.cuh"
 #include "common.cuh"
 #include "lpt.cuh"
 #include "quant.cuh"
@@ -294,34 +294,29 @@ int attend_tiles(const AttendLaunch &a, cudaStream_t s) {
     if (!make_map(&mk, ws + w.K, BH, static_cast<int>(w.cap), d, 128) ||
         !make_map(&mv, ws + w.V, BH, static_cast<int>(w.cap), d, 128))
         return FVATTN_ERR_CUDA;
-    int32_t *nan_first = reinterpret_cast<int32_t *>(ws + w.nan_first);
-    int rc = from_cuda(cudaMemsetAsync(ws, 0, w.zero_bytes, s));
-    if (rc != FVATTN_OK) return rc;
-    if ((rc = from_cuda(launch_cache_expand(a, w.cap, ws + w.K, ws + w.V, nan_first, s))) != FVATTN_OK) return rc;
     CacheTiles ct{};
-    ct.lens = a.lens;
-    ct.new_lens = a.new_lens;
-    ct.nan_first = nan_first;
-    ct.heads = a.pool.heads;
-    ct.group = a.group;
-    ct.M = a.M;
+    ct.a = a;
+    ct.cap = w.cap;
+    ct.K = ws + w.K;
+    ct.V = ws + w.V;
+    ct.nan_first = reinterpret_cast<int32_t *>(ws + w.nan_first);
     ct.rows = static_cast<int>(attend_rows(a.group, a.M));
     ct.row_tiles = static_cast<int>(ceil_div(ct.rows, 128));
-    ct.causal = a.causal;
-    ct.cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
-    ct.q_b = a.q_b, ct.q_h = a.q_h, ct.q_n = a.q_n;
-    ct.o_b = a.o_b, ct.o_h = a.o_h, ct.o_n = a.o_n;
+    const int64_t items = BH * ct.row_tiles;
+    ct.ctas = a.sms;  // of the attention kernel: one an SM
+    ct.n_rest = static_cast<int>(items % ct.ctas);
+    ct.n_whole = static_cast<int>(items - ct.n_rest);
+    ct.rest = reinterpret_cast<int32_t *>(ws + w.rest);
+    ct.part_stats = reinterpret_cast<float2 *>(ws + w.part_stats);
+    ct.part_acc = reinterpret_cast<float *>(ws + w.part_acc);
+    int rc = from_cuda(cudaMemsetAsync(ws, 0, w.zero_bytes, s));
+    if (rc != FVATTN_OK) return rc;
+    if ((rc = from_cuda(launch_cache_expand(ct, s))) != FVATTN_OK) return rc;
     AttnLaunch l{};
     l.Q = a.Q;
     l.tmap_k = &mk;
     l.tmap_v = &mv;
-    const int64_t items = BH * ct.row_tiles;
-    const int grid = a.sms;  // CTAs of the attention kernel: one an SM
-    ct.n_rest = static_cast<int>(items % grid);
-    ct.rest = reinterpret_cast<int32_t *>(ws + w.rest);
-    ct.part_stats = reinterpret_cast<float2 *>(ws + w.part_stats);
-    ct.part_acc = reinterpret_cast<float *>(ws + w.part_acc);
-    l.n_items = static_cast<int>(items - ct.n_rest);
+    l.n_items = ct.n_whole;
     l.work_counter = reinterpret_cast<int *>(ws + w.counter);
     l.N = static_cast<int>(w.cap);
     l.nb = static_cast<int>(w.cap / 128);

@@ -29,24 +29,7 @@ struct AttnLaunch {
     const int32_t *q_exp, *k_exp, *v_exp;
 };
 
-// Dense attention of many new query rows per sequence over cached keys and values that
-// lie expanded as bf16 [B * heads, cap, d] (the tensor maps of AttnLaunch, boxes of 128
-// tokens): what the kernel needs instead of a CSR.  Rows of one key head are its `group`
-// query heads times M new tokens; an item is 128 of them.  The first n_items items (a multiple of the
-// grid) come whole from the queue, in order, so that the SMs share one head's keys in L2; the
-// n_rest behind them, fewer than the grid, are cut into equal stretches of key tiles, one a
-// CTA, and joined (a last wave of whole items would leave most SMs idle).
-struct CacheTiles {
-    int32_t *rest;       // [n_rest + 1] key tiles before each of the rest (cache_rest_kernel)
-    float2 *part_stats;  // [2 * grid, 128] m, l of the partial rows
-    float *part_acc;     // [2 * grid, 128, d]
-    int n_rest;
-    const int32_t *lens, *new_lens;  // per sequence: cached tokens, new ones (null: all M)
-    const int32_t *nan_first;        // [B * heads, d]: 2^31 - 1 - first token whose V was NaN there, 0 none
-    int heads, group, M, rows, row_tiles, causal;
-    int64_t cap;
-    int64_t q_b, q_h, q_n, o_b, o_h, o_n;  // strides of Q and O, in elements
-};
+struct CacheTiles;  // cache_tiles.cuh
 
 int attn_smem_bytes(int d, int bs);
 // Work items of the attention kernel: the CSR rows (query blocks of every head) at

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "cache_index.h"
+#include "common.cuh"
 #include "rope.cuh"
 
 namespace fvattn {
@@ -59,12 +60,6 @@ inline int64_t attend_rows(int group, int M) { return static_cast<int64_t>(group
 bool attend_few_rows(int group, int M);
 size_t attend_few_workspace(int B, int d, int sms);
 cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream);
-// Pages of every sequence as bf16 K and V [B * heads, cap, d] (zeros from the sequence's end
-// to the next multiple of 128 tokens), and the calls' device checks.  nan_first: int32 [B * heads,
-// d], zeroed before; gets 2^31 - 1 - t for the first token t whose V is NaN in that channel.
-cudaError_t launch_cache_expand(const AttendLaunch &a, int64_t cap, void *K, void *V, int32_t *nan_first,
-                                cudaStream_t stream);
-
 #ifdef __CUDACC__
 
 // x * 2^e for |e| up to 252: two exact factors (a single 2^e may lie outside fp32).  Exact
@@ -78,6 +73,56 @@ __device__ __forceinline__ int clamp_exp(int e) { return max(-250, min(e, 250));
 // Whether any of the four e4m3 codes of w is a NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool any_nan_e4m3(uint32_t w) {
     return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
+
+struct Seq {
+    int len;    // cached tokens (a page table holds fewer than 2^31)
+    int n_new;  // of them new: the queries
+};
+
+__device__ __forceinline__ Seq sequence(const AttendLaunch &a, int b) {
+    const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
+    Seq s;
+    s.len = static_cast<int>(clamp_len(a.lens[b], cap));
+    s.n_new = static_cast<int>(clamp_len(a.new_lens ? a.new_lens[b] : a.M, a.M));
+    return s;
+}
+
+// Tokens that query token m sees: [0, limit).
+__device__ __forceinline__ int row_limit(const AttendLaunch &a, const Seq &s, int m) {
+    if (m >= s.n_new) return 0;
+    return a.causal ? static_cast<int>(clamp_len(static_cast<int64_t>(s.len) - s.n_new + m + 1, s.len)) : s.len;
+}
+
+// Lengths, counts and the page table entries in use; one CTA, writes the status word.
+__device__ __forceinline__ void check_attend(const AttendLaunch &a) {
+    const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
+    bool bad = false;
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const int64_t len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.M;
+        if (len < 0 || len > cap || n < 0 || n > a.M) bad = true;
+    }
+    const int all = a.B * a.pool.max_pages, stride = static_cast<int>(blockDim.x);
+    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * stride) {
+        int page[4];
+        int64_t len[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // four entries' loads at a time
+            const int i = i0 + k * stride;
+            page[k] = i < all ? __ldg(a.pool.table + i) : 0;
+            len[k] = i < all ? __ldg(a.lens + i / a.pool.max_pages) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * stride;
+            if (i < all && static_cast<int64_t>(i % a.pool.max_pages) * a.pool.block < clamp_len(len[k], cap) &&
+                checked_page(page[k], a.pool.num_pages) < 0)
+                bad = true;
+        }
+        if (all - i0 <= 4 * stride) break;  // i0 + 4 stride may pass 2^31
+    }
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *a.dev_status = any ? FVATTN_ERR_BAD_PAGE : FVATTN_OK;
 }
 
 #endif

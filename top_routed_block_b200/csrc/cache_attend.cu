@@ -48,10 +48,11 @@
 // at most 512 tokens take one CTA a segment and one launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <atomic>
 #include <cstdint>
 #include <math_constants.h>
 
-#include "cache.cuh"
+#include "cache_tiles.cuh"
 #include "common.cuh"
 
 namespace fvattn {
@@ -142,56 +143,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-struct Seq {
-    int len;    // cached tokens (a page table holds fewer than 2^31)
-    int n_new;  // of them new: the queries
-};
-
-__device__ __forceinline__ Seq sequence(const AttendLaunch &a, int b) {
-    const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
-    Seq s;
-    s.len = static_cast<int>(clamp_len(a.lens[b], cap));
-    s.n_new = static_cast<int>(clamp_len(a.new_lens ? a.new_lens[b] : a.M, a.M));
-    return s;
-}
-
-// Tokens that query token m sees: [0, limit).
-__device__ __forceinline__ int row_limit(const AttendLaunch &a, const Seq &s, int m) {
-    if (m >= s.n_new) return 0;
-    return a.causal ? static_cast<int>(clamp_len(static_cast<int64_t>(s.len) - s.n_new + m + 1, s.len)) : s.len;
-}
-
-// Lengths, counts and the page table entries in use; one CTA, writes the status word.
-__device__ void check_attend(const AttendLaunch &a) {
-    const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
-    bool bad = false;
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const int64_t len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.M;
-        if (len < 0 || len > cap || n < 0 || n > a.M) bad = true;
-    }
-    const int all = a.B * a.pool.max_pages, stride = static_cast<int>(blockDim.x);
-    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * stride) {
-        int page[4];
-        int64_t len[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // four entries' loads at a time
-            const int i = i0 + k * stride;
-            page[k] = i < all ? __ldg(a.pool.table + i) : 0;
-            len[k] = i < all ? __ldg(a.lens + i / a.pool.max_pages) : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = i0 + k * stride;
-            if (i < all && static_cast<int64_t>(i % a.pool.max_pages) * a.pool.block < clamp_len(len[k], cap) &&
-                checked_page(page[k], a.pool.num_pages) < 0)
-                bad = true;
-        }
-        if (all - i0 <= 4 * stride) break;  // i0 + 4 stride may pass 2^31
-    }
-    const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *a.dev_status = any ? FVATTN_ERR_BAD_PAGE : FVATTN_OK;
 }
 
 // ------------------------------------------------------------------ the plan
@@ -787,13 +738,22 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
 // nan_first, so that a NaN that a query does not see cannot reach it through 0 * NaN.
 constexpr int kExpandThreads = 256;
 
-struct ExpandArgs {
-    AttendLaunch a;
-    int64_t cap;
-    __nv_bfloat16 *K, *V;
-    int32_t *nan_first;
-    int pages;
-};
+// By the checking CTA: key tiles (at least one each) before each of the rest items.
+__device__ void plan_rest(const CacheTiles &ct) {
+    __shared__ int sums[kExpandThreads];
+    const int i = static_cast<int>(threadIdx.x);  // (there are fewer of them than SMs)
+    const int n = i < ct.n_rest ? max(cache_tiles_of(ct, ct.n_whole + i), 1) : 0;
+    sums[i] = n;
+    __syncthreads();
+    for (int o = 1; o < kExpandThreads; o <<= 1) {
+        const int t = i >= o ? sums[i - o] : 0;
+        __syncthreads();
+        sums[i] += t;
+        __syncthreads();
+    }
+    if (i < ct.n_rest) ct.rest[i] = sums[i] - n;
+    if (i == 0) ct.rest[ct.n_rest] = sums[kExpandThreads - 1];
+}
 
 // Eight codes times 2^e (f, where that is a normal number).
 __device__ __forceinline__ uint4 expand8(uint2 codes, int e, bool plain, float f) {
@@ -811,16 +771,18 @@ __device__ __forceinline__ uint4 expand8(uint2 codes, int e, bool plain, float f
 }
 
 template <int D>
-__global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __grid_constant__ ExpandArgs g) {
+__global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __grid_constant__ CacheTiles ct) {
     constexpr int PER_ROW = D / 8, AHEAD = 64 * PER_ROW / kExpandThreads;  // a vector: 8 codes; 64 rows at a time
-    const AttendLaunch &a = g.a;
+    const AttendLaunch &a = ct.a;
     if (blockIdx.x == 0) {
+        plan_rest(ct);
         check_attend(a);
         return;
     }
+    const int pages = static_cast<int>(ct.cap / a.pool.block);
     int64_t x = static_cast<int64_t>(blockIdx.x) - 1;
-    const int pg = static_cast<int>(x % g.pages);
-    x /= g.pages;
+    const int pg = static_cast<int>(x % pages);
+    x /= pages;
     const int h = static_cast<int>(x % a.pool.heads);
     const int b = static_cast<int>(x / a.pool.heads);
     const int BS = a.pool.block;
@@ -841,7 +803,7 @@ __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __gr
         const bool plain = e >= -126 && e <= 127;
         const float f = plain ? __int_as_float((e + 127) << 23) : 0.0f;
         const uint2 *src = reinterpret_cast<const uint2 *>((is_v ? a.pool.v : a.pool.k) + (ph * BS + row0) * D);
-        uint4 *dst = reinterpret_cast<uint4 *>((is_v ? g.V : g.K) + (bh * g.cap + tok0 + row0) * D);
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(is_v ? ct.V : ct.K) + (bh * ct.cap + tok0 + row0) * D);
         uint2 c[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
@@ -857,7 +819,7 @@ __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __gr
                     const int sh = (y & 3) * 8;
                     if (((word >> sh) & 0x7fu) != 0x7fu) continue;
                     word &= ~(0xffu << sh);
-                    atomicMax(g.nan_first + bh * D + at % PER_ROW * 8 + y, 0x7fffffff - (tok0 + row0 + at / PER_ROW));
+                    atomicMax(ct.nan_first + bh * D + at % PER_ROW * 8 + y, 0x7fffffff - (tok0 + row0 + at / PER_ROW));
                 }
             }
             dst[at] = expand8(c[i], e, plain, f);
@@ -879,22 +841,23 @@ static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
     const AttendLaunch &a = g.a;
     constexpr size_t steps = static_cast<size_t>(kWarps) * 2 * Step<D>::BYTES;
     const size_t smem = steps + (2 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-    // (per device and call: the attribute belongs to the device's own copy of the function)
-    cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
+    // (the attribute belongs to the device's own copy of the function: set on its first call)
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {
+        e = cudaFuncSetAttribute(attend_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit);
+    }
     attend_few_kernel<D><<<static_cast<unsigned>(g.ctas) + 1, kThreads, smem, stream>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess || g.whole) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.pool.heads * attend_rows(a.group, a.M)), static_cast<unsigned>(a.B));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
+    cudaLaunchConfig_t cfg = early_launch(
+        dim3(static_cast<unsigned>(a.pool.heads * attend_rows(a.group, a.M)), static_cast<unsigned>(a.B)), kJoinThreads, 0, stream);
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, g);
 }
 
@@ -915,13 +878,11 @@ cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream) {
     return a.pool.d == 128 ? launch_few_t<128>(g, stream) : launch_few_t<64>(g, stream);
 }
 
-cudaError_t launch_cache_expand(const AttendLaunch &a, int64_t cap, void *K, void *V, int32_t *nan_first,
-                                cudaStream_t stream) {
-    ExpandArgs g{a, cap, static_cast<__nv_bfloat16 *>(K), static_cast<__nv_bfloat16 *>(V), nan_first,
-                 static_cast<int>(cap / a.pool.block)};
-    const int64_t ctas = static_cast<int64_t>(a.B) * a.pool.heads * g.pages + 1;
-    if (a.pool.d == 128) cache_expand_kernel<128><<<static_cast<unsigned>(ctas), kExpandThreads, 0, stream>>>(g);
-    else cache_expand_kernel<64><<<static_cast<unsigned>(ctas), kExpandThreads, 0, stream>>>(g);
+cudaError_t launch_cache_expand(const CacheTiles &ct, cudaStream_t stream) {
+    const AttendLaunch &a = ct.a;
+    const unsigned ctas = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.pool.heads * (ct.cap / a.pool.block) + 1);
+    if (a.pool.d == 128) cache_expand_kernel<128><<<ctas, kExpandThreads, 0, stream>>>(ct);
+    else cache_expand_kernel<64><<<ctas, kExpandThreads, 0, stream>>>(ct);
     return cudaGetLastError();
 }
 

@@ -33,6 +33,25 @@ struct Carver {
     }
 };
 
+// A launch that may begin before the kernel in front of it in the stream has ended: the kernel waits for
+// that one's results itself (griddepcontrol.wait).
+inline cudaLaunchConfig_t early_launch(dim3 grid, unsigned threads, size_t smem, cudaStream_t stream) {
+    static cudaLaunchAttribute early = [] {
+        cudaLaunchAttribute a{};
+        a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        a.val.programmaticStreamSerializationAllowed = 1;
+        return a;
+    }();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 constexpr int kMaxRouteBlocks = 1024;   // routing keeps one row's scores in shared memory
 constexpr int kMaxCount = 4096;         // largest key-block count a row may hold
 constexpr int kMaxHeads = 4096;         // largest B*H of the attention call (head ordering in one CTA)
