@@ -39,13 +39,15 @@
 // whole lines they reach 6.8: a copy loop alone, 900 MB of pages in random order.)
 //
 // Split: the work is planned on the device from the lengths, so that the host never waits for
-// them.  A segment is one (sequence, key head, row tile), its units 256 tokens.  Much work (8 units
-// for each resident CTA, or more): the line of all segments' units is cut into equal
-// stretches, one a CTA; it does whole segments in passing and leaves partials of the two it
-// shares with its neighbours.  Little work: each segment is cut into its own chunks, as
-// small as the resident CTAs allow, one a CTA, because beginning a segment costs as much as two
-// units.  A second kernel joins partials in order: no atomics, the same bits every time.  Caches of
-// at most 512 tokens take one CTA a segment and one launch.
+// them.  A segment is one (sequence, key head), its units the tokens that a CTA's warps take at
+// once.  Much work (8 units for each resident CTA, or more): the line of all segments' units is cut
+// into equal stretches; a CTA does whole segments in passing and leaves partials of the two it
+// shares with its neighbours.  Little work: each segment is cut into its own chunks, as small as
+// the resident CTAs allow, one a CTA, because beginning a segment costs as much as two units.  With
+// several row tiles each stretch or chunk goes to as many neighbouring CTAs, which read the
+// same tokens at about the same time: from HBM once.  A second kernel joins partials in order: no
+// atomics, the same bits every time.  Caches of at most 512 tokens take one CTA a segment and row
+// tile, and one launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <atomic>
@@ -62,8 +64,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;                // rows of a tile
-constexpr int kStep = 64;               // tokens a warp takes at a time (inside one page: pages hold 64 or 128)
-constexpr int kUnit = kStep * kWarps;   // tokens a CTA takes at a time
+// Tokens a warp takes at a time (inside one page: pages hold 64 or 128); a unit is what the CTA's
+// warps take.  One row tile, bound by HBM: 32, whose finer cut of the work balances better (8 x 40
+// heads, 88 k tokens, d 128: 141 us, with 64 149).  More tiles, bound by the warps: 64, which
+// spends less on each token (20 rows, 4 x 8 heads, 20 k tokens: 27 us, with 32 34).
+constexpr int kOneTileStep = 32, kMoreTilesStep = 64;
 constexpr int kWholeTokens = 512;       // caches this short: a CTA takes a whole segment
 constexpr int kCtasPerSm = 3;           // by shared memory (64 KB each at d 128) and registers
 constexpr int kChunkShare = 8;          // units per CTA below which segments are cut into chunks
@@ -89,12 +94,13 @@ FewWorkspace few_layout(int B, int d, int ctas) {
 struct FewArgs {
     AttendLaunch a;
     int32_t *plan;    // [B + 2] the plan, from CTA 0 for the joining kernel
+    int unit;         // tokens
     float4 *stats;    // [2 * ctas, kRows]: m, l, w
     float *acc;       // [2 * ctas, kRows, d]
     float scale_log2;
     int row_tiles;
-    int ctas;         // that take work
-    bool whole;       // a CTA per segment
+    int ctas;         // stretches of the work; each is done by row_tiles neighbouring CTAs
+    bool whole;       // a CTA per segment and row tile
     int log2_block;
 };
 
@@ -147,7 +153,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // ------------------------------------------------------------------ the plan
 
-__device__ __forceinline__ int units_of(int len) { return static_cast<int>(segment_units(len, kUnit)); }
+__device__ __forceinline__ int units_of(const FewArgs &g, int len) {
+    return static_cast<int>(segment_units(len, g.unit));
+}
 
 // The plan, in shared memory: first[b] = what comes before sequence b, for b = 0 .. B, in units
 // (stretches) or in chunks of at most first[B + 1] units; first[B + 1] = 0 says stretches.
@@ -157,11 +165,11 @@ __device__ void make_plan(const FewArgs &g, int *first, int *lens) {
     const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const int groups = a.pool.heads * g.row_tiles;
+        const int groups = a.pool.heads;
         int total = 0;
         for (int b = lane; b < a.B; b += 32) {
             lens[b] = static_cast<int>(clamp_len(a.lens[b], cap));
-            total += units_of(lens[b]) * groups;
+            total += units_of(g, lens[b]) * groups;
         }
         total = __reduce_add_sync(0xffffffffu, total);
         __syncwarp();
@@ -169,14 +177,14 @@ __device__ void make_plan(const FewArgs &g, int *first, int *lens) {
         int chunk = 0;
         if (total < kChunkShare * g.ctas && a.B <= kChunkSequences) {
             int n = 0;
-            for (int b = 0; b < a.B; ++b) n += (units_of(lens[b]) + lane) / (lane + 1);
+            for (int b = 0; b < a.B; ++b) n += (units_of(g, lens[b]) + lane) / (lane + 1);
             const uint32_t fits = __ballot_sync(0xffffffffu, n * groups <= g.ctas);
             chunk = __ffs(static_cast<int>(fits));  // 0: none
         }
         int before = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
-            const int u = b < a.B ? units_of(lens[b]) : 0;
+            const int u = b < a.B ? units_of(g, lens[b]) : 0;
             const int n = (chunk ? (u + chunk - 1) / chunk : u) * groups;
             int inc = n;
 #pragma unroll
@@ -253,9 +261,9 @@ __device__ __forceinline__ void write_row(const AttendLaunch &a, int b, int h, i
 // A warp's part of shared memory: a step of K, then one of V, rows in order.  The 16-byte chunks of
 // each 128-byte line (one row at d 128, two at d 64) are permuted by exclusive or with a number
 // that depends on the line.
-template <int D>
+template <int D, int STEP>
 struct Step {
-    static constexpr int BYTES = kStep * D;
+    static constexpr int BYTES = STEP * D;
 
     // K's reads take 4 chunks of two neighbouring rows at a time, V's two chunks of every other row
     // of 8 (d 64: half rows): both hit 8 different chunk places.
@@ -288,13 +296,14 @@ __device__ __forceinline__ void copies_wait() {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int D>
+template <int D, int STEP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const __grid_constant__ FewArgs g) {
     constexpr int KW = D / 16;      // words of a lane's part of a query or key row
     constexpr int MT = D / 16;      // m16 tiles of V^T P^T
     constexpr int VW = D / 32;      // words of a lane's V row
-    constexpr int ST = kStep / 16;  // 16-token tiles of a step
-    using S_ = Step<D>;
+    constexpr int ST = STEP / 16;   // 16-token tiles of a step
+    constexpr int UNIT = STEP * kWarps;
+    using S_ = Step<D, STEP>;
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char *kr = smem + (threadIdx.x >> 5) * 2 * S_::BYTES, *vr = kr + S_::BYTES;  // this warp's K and V
     float *acc_s = reinterpret_cast<float *>(smem);  // [kWarps][kRows][D], between segments
@@ -303,7 +312,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
     __shared__ float4 stat_s[kWarps][kRows];
     static_assert(kRows * D * 4 <= 2 * S_::BYTES, "the sums reuse the steps' place");
     const AttendLaunch &a = g.a;
-    const int groups = a.pool.heads * g.row_tiles;
     if (!g.whole) make_plan(g, first, lens);
     if (blockIdx.x == 0) {
         if (!g.whole)
@@ -318,49 +326,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
     const int cta = static_cast<int>(blockIdx.x) - 1;
     const uint32_t k_at = static_cast<uint32_t>(__cvta_generic_to_shared(kr)), v_at = k_at + S_::BYTES;
 
-    int unit = cta, unit_end = cta + 1, chunk = 0;
+    const int rt = cta % g.row_tiles, stretch = cta / g.row_tiles;
+    const int row0 = rt * kRows, rows = min(kRows, R - row0);
+    int unit = stretch, unit_end = stretch + 1, chunk = 0;
     if (!g.whole) {
         const int total = first[a.B];
         chunk = first[a.B + 1];
         const int n = stretches(total, g.ctas);
-        if (cta >= n) return;
+        if (stretch >= n) return;
         if (!chunk) {
-            unit = static_cast<int>(stretch_start(cta, total, n));
-            unit_end = static_cast<int>(stretch_start(cta + 1, total, n));
+            unit = static_cast<int>(stretch_start(stretch, total, n));
+            unit_end = static_cast<int>(stretch_start(stretch + 1, total, n));
         }
     }
     while (unit < unit_end) {
         // the segment, and units [off, off + n_units) of its
-        int b, seg, off = 0, n_units, all;
+        int b, h, off = 0, n_units, all;
         Seq seq;
         if (g.whole) {
-            b = cta / groups;
-            seg = cta % groups;
+            b = stretch / H;
+            h = stretch % H;
             seq = sequence(a, b);
-            n_units = all = units_of(seq.len);
+            n_units = all = units_of(g, seq.len);
             unit = unit_end;
         } else {
             b = find_sequence(first, a.B, unit);
             seq = Seq{lens[b], a.new_lens ? static_cast<int>(clamp_len(__ldg(a.new_lens + b), a.M)) : a.M};
-            all = units_of(seq.len);
+            all = units_of(g, seq.len);
             const int at = unit - first[b];
             if (chunk) {  // its chunks are as even as can be
                 const int n = (all + chunk - 1) / chunk;
-                seg = at / n;
+                h = at / n;
                 off = static_cast<int>(stretch_start(at % n, all, n));
                 n_units = static_cast<int>(stretch_start(at % n + 1, all, n)) - off;
                 unit = unit_end;
             } else {
-                seg = at / all;
+                h = at / all;
                 off = at % all;
                 n_units = min(all - off, unit_end - unit);
                 unit += n_units;
             }
         }
-        const int h = seg / g.row_tiles, row0 = seg % g.row_tiles * kRows;
-        const int rows = min(kRows, R - row0);
 
-        const int c1 = seq.n_new == 0 ? 0 : min(seq.len, (off + n_units) * kUnit);
+        const int c1 = seq.n_new == 0 ? 0 : min(seq.len, (off + n_units) * UNIT);
         const int32_t *table = a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages;
         // the page and head of the step at `tok`, or -1: behind the end, or an entry outside the pool
         auto page_at = [&](int tok) -> int64_t {
@@ -369,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             return p < 0 ? -1 : static_cast<int64_t>(p) * H + h;
         };
         // this warp's step at tok is on its way (copy groups K, V); the page of the next is looked up
-        int tok = off * kUnit + warp * kStep;
-        int64_t ph = page_at(tok), ph_next = page_at(tok + kUnit);
+        int tok = off * UNIT + warp * STEP;
+        int64_t ph = page_at(tok), ph_next = page_at(tok + UNIT);
         int ek = 0, ev = 0;
         {
             const int64_t at = (ph * BS + (tok & (BS - 1))) * D;
@@ -460,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
 
-        for (; tok < c1; tok += kUnit) {
+        for (; tok < c1; tok += UNIT) {
             const bool here = ph >= 0, more = ph_next >= 0;
-            const int64_t at_next = (ph_next * BS + ((tok + kUnit) & (BS - 1))) * D;
+            const int64_t at_next = (ph_next * BS + ((tok + UNIT) & (BS - 1))) * D;
             const int ek_here = clamp_exp(ek);
             const float evf = static_cast<float>(clamp_exp(ev));
             if (more) {
@@ -470,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
                 ev = __ldg(a.pool.ve + ph_next);
             }
             ph = ph_next;
-            ph_next = page_at(tok + 2 * kUnit);
+            ph_next = page_at(tok + 2 * UNIT);
             copies_wait<1>();  // K of this step
             if (!here) {       // an entry outside the pool: its tokens are left out
                 copies_wait<0>();
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             __syncwarp();  // read by all lanes
             if (more) S_::copy(k_at, a.pool.k + at_next, lane);
             copies_commit();
-            const bool edge = tok + kStep > min_lim;
+            const bool edge = tok + STEP > min_lim;
             // the weights, transposed into the B operand
             float alpha[2];
             bool moved = false;
@@ -576,9 +584,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
 #pragma unroll
                 for (int byte = 0; byte < D / 8; ++byte) {
                     const int at = lg * (D / 8) + byte;
-                    int seen = kStep;
+                    int seen = STEP;
 #pragma unroll 1
-                    for (int row = 2 * lq; row < kStep; row += (row & 1) ? 7 : 1) {  // this lane's: 2q, 2q + 1 of each 8
+                    for (int row = 2 * lq; row < STEP; row += (row & 1) ? 7 : 1) {  // this lane's: 2q, 2q + 1 of each 8
                         unsigned char &code = vr[S_::place(row, at & ~7) + (at & 7)];
                         if ((code & 0x7fu) != 0x7fu) continue;
                         code = 0;
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
                     seen = min(seen, __shfl_xor_sync(0xffffffffu, seen, 2));
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (seen < kStep && tok + seen < lim[e]) o[byte / 2][(byte & 1) * 2 + e] = CUDART_NAN_F;
+                        if (seen < STEP && tok + seen < lim[e]) o[byte / 2][(byte & 1) * 2 + e] = CUDART_NAN_F;
                 }
             }
             // O^T += V^T P^T
@@ -684,22 +692,24 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
     const int h = blockIdx.x / R, r = blockIdx.x % R;
     const Seq seq = sequence(a, b);
     if (r % a.M >= seq.n_new) return;
-    const int total = g.plan[a.B], before = g.plan[b], chunk = g.plan[a.B + 1], units = units_of(seq.len);
-    const int seg = h * g.row_tiles + r / kRows;
-    // CTAs from..: a segment's first part is the second partial of its CTA (of the segment that CTA
+    const int total = g.plan[a.B], before = g.plan[b], chunk = g.plan[a.B + 1], units = units_of(g, seq.len);
+    const int rt = r / kRows;
+    // stretches from..: a segment's first part is the second partial of its CTA (of the segment that CTA
     // ends in), the others are the first of theirs
     int from, n_parts;
     if (chunk) {
         n_parts = (units + chunk - 1) / chunk;
-        from = before + seg * n_parts;
+        from = before + h * n_parts;
     } else {
         const int n = stretches(total, g.ctas);
-        const int64_t u0 = before + static_cast<int64_t>(seg) * units;
+        const int64_t u0 = before + static_cast<int64_t>(h) * units;
         from = stretch_of(u0, total, n);
         n_parts = stretch_of(u0 + units - 1, total, n) - from + 1;
     }
     if (n_parts <= 1) return;  // finished where it lies
-    auto part = [&](int c) { return (static_cast<int64_t>(2 * (from + c)) + (c == 0 ? 1 : 0)) * kRows + r % kRows; };
+    auto part = [&](int c) {
+        return (2 * (static_cast<int64_t>(from + c) * g.row_tiles + rt) + (c == 0 ? 1 : 0)) * kRows + r % kRows;
+    };
     const int grp = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * 4;
     Joined j;
     for (int c = grp; c < n_parts; c += GROUPS) j.top(g.stats[part(c)].x);
@@ -836,10 +846,10 @@ bool attend_few_rows(int group, int M) { return attend_rows(group, M) <= 32; }
 
 size_t attend_few_workspace(int B, int d, int sms) { return few_layout(B, d, few_ctas(sms)).total; }
 
-template <int D>
+template <int D, int STEP>
 static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
     const AttendLaunch &a = g.a;
-    constexpr size_t steps = static_cast<size_t>(kWarps) * 2 * Step<D>::BYTES;
+    constexpr size_t steps = static_cast<size_t>(kWarps) * 2 * Step<D, STEP>::BYTES;
     const size_t smem = steps + (2 * static_cast<size_t>(a.B) + 2) * sizeof(int);
     // (the attribute belongs to the device's own copy of the function: set on its first call)
     static std::atomic<uint64_t> ready{0};
@@ -848,12 +858,12 @@ static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
-        e = cudaFuncSetAttribute(attend_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attend_few_kernel<D, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit);
     }
-    attend_few_kernel<D><<<static_cast<unsigned>(g.ctas) + 1, kThreads, smem, stream>>>(g);
+    attend_few_kernel<D, STEP><<<static_cast<unsigned>(g.ctas * g.row_tiles) + 1, kThreads, smem, stream>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess || g.whole) return e;
     cudaLaunchConfig_t cfg = early_launch(
@@ -868,14 +878,18 @@ cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream) {
     g.whole = static_cast<int64_t>(a.pool.max_pages) * a.pool.block <= kWholeTokens;
     const int most = few_ctas(a.sms);
     const FewWorkspace w = few_layout(a.B, a.pool.d, most);
-    g.ctas = g.whole ? a.B * a.pool.heads * g.row_tiles : most;
+    g.ctas = g.whole ? a.B * a.pool.heads : most / g.row_tiles;
+    const int step = g.row_tiles == 1 ? kOneTileStep : kMoreTilesStep;
+    g.unit = step * kWarps;
     g.log2_block = a.pool.block == 128 ? 7 : 6;
     char *ws = static_cast<char *>(a.workspace);
     g.plan = reinterpret_cast<int32_t *>(ws + w.plan);
     g.stats = reinterpret_cast<float4 *>(ws + w.stats);
     g.acc = reinterpret_cast<float *>(ws + w.acc);
     g.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.pool.d)));
-    return a.pool.d == 128 ? launch_few_t<128>(g, stream) : launch_few_t<64>(g, stream);
+    if (a.pool.d == 128)
+        return g.row_tiles == 1 ? launch_few_t<128, kOneTileStep>(g, stream) : launch_few_t<128, kMoreTilesStep>(g, stream);
+    return g.row_tiles == 1 ? launch_few_t<64, kOneTileStep>(g, stream) : launch_few_t<64, kMoreTilesStep>(g, stream);
 }
 
 cudaError_t launch_cache_expand(const CacheTiles &ct, cudaStream_t stream) {
