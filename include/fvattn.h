@@ -522,9 +522,9 @@ FVATTN_API int fvattn_cache_append(const void *K, const int64_t *k_strides, cons
                                    int64_t pos_batch_stride, const double *inv_freq, const int32_t *pair_axis,
                                    int n_pairs, int n_axes, int pairing, int32_t *dev_status, fvattn_stream_t stream);
 
-/* Device workspace fvattn_cache_attend needs, in bytes (0 on bad arguments).  Up to 32 rows
- * (group * M) it holds the partial results of the split; above, the pages as bf16
- * (B * heads * max_pages * block * d * 4 bytes). */
+/* Device workspace fvattn_cache_attend needs, in bytes (0 on bad arguments).  Up to 64 rows
+ * (group * M; 128 with max_pages * block <= 512) it holds the partial results of the split; above,
+ * the pages as bf16 (B * heads * max_pages * block * d * 4 bytes) and partial results. */
 FVATTN_API size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block,
                                                       int max_pages);
 
@@ -540,15 +540,15 @@ FVATTN_API size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int grou
  *   LSE           out, fp32 [B, heads * group, M], natural logarithm.
  * A query that sees no token (an empty sequence) gets O = 0 and LSE = -inf.  What a query does
  * not see, NaN codes and places behind the sequence's end among it, does not reach its row.
- * Up to 32 rows (group * M): the weights are rounded to fp16 before P V and the cached tokens
- * are split over the SMs and joined in a fixed order.  Above: the pages are expanded to bf16
- * (exact) in the workspace and the tensor cores' 128-row tiles run over them, with P rounded to
- * bf16 as in fvattn_sparse_fwd.  Both sum in fp32.  The result does not depend on what else
- * runs; no atomics on floating values.
+ * Few rows (as above): the weights are rounded to fp16 before P V and the cached tokens are
+ * split over the SMs and joined in a fixed order.  More: the pages are expanded to bf16 (exact) in
+ * the workspace and the tensor cores' 128-row tiles run over them, with P rounded to bf16 as in
+ * fvattn_sparse_fwd.  Both sum in fp32.  The result does not depend on what else runs; no atomics
+ * on floating values.  Exponents outside [-250, 250] are taken as the nearer end.
  * *dev_status (written by the call): FVATTN_ERR_BAD_PAGE where lens is outside [0, max_pages *
  * block], new_lens outside [0, M] (both are clamped), or an entry of the page table in use is
- * outside [0, num_pages) (above 32 rows its tokens count as zeros, up to 32 rows they are left out:
- * the result is not to be used); FVATTN_ERR_DEVICE_TIMEOUT as fvattn_sparse_fwd.
+ * outside [0, num_pages) (with many rows its tokens count as zeros, with few they are left out: the
+ * result is not to be used); FVATTN_ERR_DEVICE_TIMEOUT as fvattn_sparse_fwd.
  * B <= 4096; B * heads * max_pages * block / 64 < 2^31; group * M < 2^24.
  */
 FVATTN_API int fvattn_cache_attend(const void *Q, const int64_t *q_strides, int B, int heads, int group, int M, int d,

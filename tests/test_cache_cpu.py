@@ -114,8 +114,8 @@ def test_attend_workspace(lib):
     import top_routed_block_b200 as fv
     ws = fv.fvattn_cache_attend_workspace_bytes
     assert ws(0, 1, 1, 1, 64, 64, 1) == 0 and ws(1, 1, 1, 1, 96, 64, 1) == 0 and ws(4097, 1, 1, 1, 64, 64, 1) == 0
-    # more than 32 rows: K and V of every page as bf16
-    assert ws(2, 3, 4, 9, 128, 128, 5) >= 2 * 2 * 3 * 5 * 128 * 128 * 2
+    # more than 64 rows: K and V of every page as bf16
+    assert ws(2, 3, 8, 9, 128, 128, 5) >= 2 * 2 * 3 * 5 * 128 * 128 * 2
     # few rows: bounded by the grid, not by the cache's length
     assert 0 < ws(1, 8, 1, 1, 128, 128, 1 << 20) < 64 << 20
     assert 0 < ws(1, 1, 1, 1, 64, 64, 1) < 8 << 20

@@ -6,8 +6,8 @@ scale below 2^-6):
            error, see test_rope_gpu.py); an exponent may differ by one only where the largest
            magnitude is within that error of a power of two times 448.
   attend   score error e_s = (d + 16) 2^-24 sum |q||k| / sqrt(d) (fp32 sums, scale, argument of
-           the exponential); a weight's relative error w = 2^-11 (fp16, up to 32 rows) or 2^-8
-           (bf16) + 2 e_s + 2^-20 (exponentials and their rescaling) + n 2^-24 (fp32 sums over n
+           the exponential); a weight's relative error w = 2^-11 (fp16, up to 32 rows; here
+           2^-8 above) or 2^-8 (bf16) + 2 e_s + 2^-20 (exponentials and their rescaling) + n 2^-24 (fp32 sums over n
            tokens); |dO| <= w sum P|v| + 2^-8 |O|; |dLSE| <= e_s + 2^-20 + n 2^-24 + 2^-22 |LSE|."""
 import numpy as np
 import pytest

@@ -284,7 +284,7 @@ CacheTilesWorkspace cache_tiles_layout(int64_t BH, int d, int block, int max_pag
     return w;
 }
 
-// More than 32 rows: the pages as bf16, then 128-row tiles over them.
+// Many rows: the pages as bf16, then 128-row tiles over them.
 int attend_tiles(const AttendLaunch &a, cudaStream_t s) {
     const int64_t BH = static_cast<int64_t>(a.B) * a.pool.heads;
     const int d = a.pool.d;
@@ -912,7 +912,7 @@ int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, 
 
 size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block, int max_pages) {
     if (check_attend_shape(B, heads, group, M, d, block, max_pages) != FVATTN_OK) return 0;
-    if (attend_few_rows(group, M)) return attend_few_workspace(B, d, kPlanSms);
+    if (attend_few_rows(group, M, static_cast<int64_t>(max_pages) * block)) return attend_few_workspace(B, d, kPlanSms);
     return cache_tiles_layout(static_cast<int64_t>(B) * heads, d, block, max_pages).total;
 }
 
@@ -956,7 +956,7 @@ int fvattn_cache_attend(const void *Q, const int64_t *q_strides, int B, int head
     a.workspace = workspace;
     a.sms = info.sms < kPlanSms ? info.sms : kPlanSms;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return attend_few_rows(group, M) ? from_cuda(launch_attend_few(a, s)) : attend_tiles(a, s);
+    return attend_few_rows(group, M, static_cast<int64_t>(max_pages) * block) ? from_cuda(launch_attend_few(a, s)) : attend_tiles(a, s);
 }
 
 }  // extern "C"

@@ -57,7 +57,7 @@ struct AttendLaunch {
 inline int64_t attend_rows(int group, int M) { return static_cast<int64_t>(group) * M; }
 // Whether the call takes the few-rows kernel (else the pages are expanded and the tensor
 // cores' 128-row tiles run over them).
-bool attend_few_rows(int group, int M);
+bool attend_few_rows(int group, int M, int64_t capacity);
 size_t attend_few_workspace(int B, int d, int sms);
 cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream);
 #ifdef __CUDACC__

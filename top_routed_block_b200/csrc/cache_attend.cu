@@ -842,7 +842,14 @@ int few_ctas(int sms) { return sms * kCtasPerSm - 1; }
 
 }  // namespace
 
-bool attend_few_rows(int group, int M) { return attend_rows(group, M) <= 32; }
+// The few-rows kernel's time grows with its row tiles; the other one pays for expanding the pages
+// and is the same from 1 to 128 rows.  They meet at about 64 (us, few / tiles: d 128, 4 x 8 heads, 93 k
+// tokens in all: 48 rows 148 / 183, 64 rows 189 / 184, 96 rows 283 / 185; 23 k tokens: 54 / 64, 67 / 63,
+// 94 / 64; d 64, 23 k: 36 / 49, 44 / 48, 61 / 49), and at 128 where a CTA takes a whole cache and nothing
+// is joined (500 tokens: 96 rows 15 / 23, 128 rows 20 / 23).
+bool attend_few_rows(int group, int M, int64_t capacity) {
+    return attend_rows(group, M) <= (capacity <= kWholeTokens ? 128 : 64);
+}
 
 size_t attend_few_workspace(int B, int d, int sms) { return few_layout(B, d, few_ctas(sms)).total; }
 
