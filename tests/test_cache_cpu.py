@@ -241,6 +241,21 @@ def test_lanes_read_each_cached_byte_once(d, step):
         assert (hit == 1).all()
 
     lanes = [(lane >> 2, lane & 3) for lane in range(32)]
+    # the places as a lane's constant and an immediate
+    for lane, (g, q) in enumerate(lanes):
+        line = lane >> 3
+        c = chunk_place(d, line * 128 // d, (lane & 7) * 16 % d) if d == 128 else chunk_place(
+            d, line * 2 + (lane & 7) // 4, (lane & 3) * 16)
+        for i in range(step * d // 512):
+            byte = i * 512 + lane * 16
+            assert (c ^ 64 if d == 128 and i & 1 else c) + i * 512 == chunk_place(d, byte // d, byte % d)
+        k, v = chunk_place(d, g, q * 16), chunk_place(d, 2 * q, g * (d // 8))
+        for r8 in range(step // 8):
+            for half in range(d // 64):
+                assert (k ^ 64 if half else k) + r8 * 8 * d == chunk_place(d, g + 8 * r8, half * 64 + q * 16)
+            for odd in range(2):
+                want = chunk_place(d, 2 * q + odd + 8 * r8, g * (d // 8))
+                assert ((v ^ 64) + (128 if d == 128 else 0) if odd else v) + r8 * 8 * d == want
     check([[(mt * 16 + half * 8 + g, c * 64 + q * 16) for g, q in lanes] for mt in range(step // 16) for half in range(2)
            for c in range(d // 64)], 16)
     check([[(kg * 16 + (t >> 1) * 8 + (t & 1) + 2 * q, g * (d // 8)) for g, q in lanes] for kg in range(step // 16)

@@ -275,15 +275,27 @@ struct Step {
         const int byte = row * D + at, line = byte >> 7;
         return (line << 7) + ((((byte >> 4) & 7) ^ mix(line)) << 4) + (byte & 8);
     }
-    // One step of K or V from its first byte in the page.
-    static __device__ __forceinline__ void copy(uint32_t dst, const uint8_t *src, int lane) {
+    // place() as a lane's constant and an immediate.  Copy i of a step covers lines 4 i .. 4 i + 3, 8
+    // lanes each; whether i (d 128) is odd flips the chunks' upper bit.
+    static __device__ __forceinline__ int copy_lane(int lane) {
+        const int line = lane >> 3;
+        return (line << 7) + (((lane & 7) ^ mix(line)) << 4);
+    }
+    static __device__ __forceinline__ int copy_at(int c, int i) { return (D == 128 && (i & 1) ? c ^ 64 : c) + i * 512; }
+    // Rows g + 8 k, channels c * 64 + q * 16 ..: the row's last 3 bits are g's.
+    static __device__ __forceinline__ int key_lane(int g, int q) { return place(g, q * 16); }
+    static __device__ __forceinline__ int key_at(int c, int rows8, int half) { return (half ? c ^ 64 : c) + rows8 * 8 * D; }
+    // Rows 2 q + odd + 8 k, channels g * D/8 ..
+    static __device__ __forceinline__ int value_lane(int g, int q) { return place(2 * q, g * (D / 8)); }
+    static __device__ __forceinline__ int value_at(int c, int rows8, int odd) {
+        return (odd ? (c ^ 64) + (D == 128 ? 128 : 0) : c) + rows8 * 8 * D;
+    }
+    // One step of K or V from its first byte in the page (`src`: this lane's 16 bytes of the first copy).
+    static __device__ __forceinline__ void copy(uint32_t dst, const uint8_t *src, int lane_place) {
 #pragma unroll
-        for (int i = 0; i < BYTES / 512; ++i) {
-            const int line = i * 4 + (lane >> 3);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (line << 7) + (((lane & 7) ^ mix(line)) << 4)),
-                         "l"(src + i * 512 + lane * 16)
+        for (int i = 0; i < BYTES / 512; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + copy_at(lane_place, i)), "l"(src + i * 512)
                          : "memory");
-        }
     }
 };
 
@@ -324,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
     const int BS = a.pool.block, H = a.pool.heads;
     const int R = a.group * a.M;
     const int cta = static_cast<int>(blockIdx.x) - 1;
+    const int copy_place = S_::copy_lane(lane), key_place = S_::key_lane(lg, lq), value_place = S_::value_lane(lg, lq);
     const uint32_t k_at = static_cast<uint32_t>(__cvta_generic_to_shared(kr)), v_at = k_at + S_::BYTES;
 
     const int rt = cta % g.row_tiles, stretch = cta / g.row_tiles;
@@ -381,14 +394,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
         int64_t ph = page_at(tok), ph_next = page_at(tok + UNIT);
         int ek = 0, ev = 0;
         {
-            const int64_t at = (ph * BS + (tok & (BS - 1))) * D;
+            const int64_t at = (ph * BS + (tok & (BS - 1))) * D + lane * 16;
             if (ph >= 0) {
-                S_::copy(k_at, a.pool.k + at, lane);
+                S_::copy(k_at, a.pool.k + at, copy_place);
                 ek = __ldg(a.pool.ke + ph);
                 ev = __ldg(a.pool.ve + ph);
             }
             copies_commit();
-            if (ph >= 0) S_::copy(v_at, a.pool.v + at, lane);
+            if (ph >= 0) S_::copy(v_at, a.pool.v + at, copy_place);
             copies_commit();
         }
 
@@ -470,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
 
         for (; tok < c1; tok += UNIT) {
             const bool here = ph >= 0, more = ph_next >= 0;
-            const int64_t at_next = (ph_next * BS + ((tok + UNIT) & (BS - 1))) * D;
+            const int64_t at_next = (ph_next * BS + ((tok + UNIT) & (BS - 1))) * D + lane * 16;
             const int ek_here = clamp_exp(ek);
             const float evf = static_cast<float>(clamp_exp(ev));
             if (more) {
@@ -482,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             copies_wait<1>();  // K of this step
             if (!here) {       // an entry outside the pool: its tokens are left out
                 copies_wait<0>();
-                if (more) S_::copy(k_at, a.pool.k + at_next, lane);
+                if (more) S_::copy(k_at, a.pool.k + at_next, copy_place);
                 copies_commit();
-                if (more) S_::copy(v_at, a.pool.v + at_next, lane);
+                if (more) S_::copy(v_at, a.pool.v + at_next, copy_place);
                 copies_commit();
                 continue;
             }
@@ -498,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     // rows g and g + 8 of the tile, channels c * 64 + q * 16 .. + 15
-                    const uint4 x0 = *reinterpret_cast<const uint4 *>(kr + S_::place(mt * 16 + lg, c * 64 + lq * 16));
-                    const uint4 x1 = *reinterpret_cast<const uint4 *>(kr + S_::place(mt * 16 + 8 + lg, c * 64 + lq * 16));
+                    const uint4 x0 = *reinterpret_cast<const uint4 *>(kr + S_::key_at(key_place, 2 * mt, c));
+                    const uint4 x1 = *reinterpret_cast<const uint4 *>(kr + S_::key_at(key_place, 2 * mt + 1, c));
                     mma_e4m3(s[mt], x0.x, x1.x, x0.y, x1.y, qh[c * 4], qh[c * 4 + 1]);
                     mma_e4m3(lo, x0.x, x1.x, x0.y, x1.y, ql[c * 4], ql[c * 4 + 1]);
                     mma_e4m3(s[mt], x0.z, x1.z, x0.w, x1.w, qh[c * 4 + 2], qh[c * 4 + 3]);
@@ -509,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
                 for (int k = 0; k < 4; ++k) s[mt][k] = fmaf(lo[k], 0.0625f, s[mt][k]);
             }
             __syncwarp();  // read by all lanes
-            if (more) S_::copy(k_at, a.pool.k + at_next, lane);
+            if (more) S_::copy(k_at, a.pool.k + at_next, copy_place);
             copies_commit();
             const bool edge = tok + STEP > min_lim;
             // the weights, transposed into the B operand
@@ -605,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
                 uint32_t vx[4][VW];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {  // tokens 2q, 2q + 1, 2q + 8, 2q + 9 of the 16, channels g * D/8 ..
-                    const unsigned char *x = vr + S_::place(kg * 16 + (t >> 1) * 8 + (t & 1) + 2 * lq, lg * (D / 8));
+                    const unsigned char *x = vr + S_::value_at(value_place, 2 * kg + (t >> 1), t & 1);
                     if constexpr (D == 128) {
                         const uint4 y = *reinterpret_cast<const uint4 *>(x);
                         vx[t][0] = y.x, vx[t][1] = y.y, vx[t][2] = y.z, vx[t][3] = y.w;
@@ -627,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
                 }
             }
             __syncwarp();
-            if (more) S_::copy(v_at, a.pool.v + at_next, lane);
+            if (more) S_::copy(v_at, a.pool.v + at_next, copy_place);
             copies_commit();
         }
         copies_wait<0>();
