@@ -459,8 +459,9 @@ FVATTN_API int fvattn_attn_work_order(const int32_t *row_ptr, const int32_t *col
  *                 b * s[0] + h * s[1] + t * s[2] + c with the host arrays q_strides and
  *                 qr_strides (in elements, multiples of 8, not negative): a projection's
  *                 [B, N, H, d] or a fused [B, N, 3, H, d] is read in place.  Qr may be Q
- *                 with the same strides (in place); any other overlap is undefined.  The
- *                 rows of Qr must not overlap each other.
+ *                 with the same strides (in place); any other overlap between what is read and
+ *                 what is written is undefined (refused where two of the pointers are equal).
+ *                 The rows of Qr must not overlap each other.
  *   K, Kr         the same with k_heads; both null with k_heads 0 to turn one tensor.
  *   pos           device int32 [N, n_axes], or [B, N, n_axes] with pos_batch_stride =
  *                 N * n_axes (0: one for all sequences).  Any int32 value: angles are reduced in
@@ -488,8 +489,8 @@ FVATTN_API int fvattn_rope(const void *Q, const int64_t *q_strides, void *Qr, co
  *                     i * block .. i * block + block - 1, in their order.
  * block in {64, 128}, d in {64, 128}, max_pages * block < 2^30.  The caller owns the pool, hands
  * out pages and keeps the lengths.  A page may stand in several sequences' tables as long
- * as no call appends to it (appending to a page that two sequences share is undefined: copy it
- * first).  Nothing is read or written in pages that a call's lengths do not reach.
+ * as no call appends to it (appending to a page that stands in two places of the table is
+ * undefined: copy it first).  Nothing is read or written in pages that a call's lengths do not reach.
  */
 
 /*

@@ -482,6 +482,8 @@ def _native_calls():
 def _on_stream(stream, f, *args):
     """f(*args) with `stream` current, so that what it allocates belongs to that stream.  Its results
     are kept from reuse until the caller's own stream has passed them too."""
+    if args[0].device != stream.device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {args[0].device}")
     before = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
         r = f(*args)

@@ -860,6 +860,13 @@ int fvattn_rope(const void *Q, const int64_t *q_strides, void *Qr, const int64_t
         k = RopeTensor{K, Kr, k_strides[0], k_strides[1], k_strides[2], kr_strides[0], kr_strides[1], kr_strides[2],
                        k_heads};
     }
+    // in place: the same element to the same element; and nothing written where the other tensor lies
+    auto same_place = [](const RopeTensor &t, int64_t b, int64_t n) {
+        return (b == 1 || t.in_b == t.out_b) && (t.heads == 1 || t.in_h == t.out_h) && (n == 1 || t.in_n == t.out_n);
+    };
+    if ((q.in == q.out && !same_place(q, B, N)) || (k.heads && k.in == k.out && !same_place(k, B, N)))
+        return FVATTN_ERR_INVALID_ARG;
+    if (k.heads && (q.out == k.out || q.out == k.in || k.out == q.in)) return FVATTN_ERR_INVALID_ARG;
     DeviceInfo info;
     if ((rc = check_device()) != FVATTN_OK) return rc;
     if (!device_info(&info)) return FVATTN_ERR_CUDA;

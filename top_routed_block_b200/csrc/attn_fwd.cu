@@ -66,6 +66,7 @@
 //     multiplies by 2^E / l.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 #include <math_constants.h>
 
@@ -1100,9 +1101,14 @@ cudaError_t launch_natural_order(int64_t n, int32_t *order, cudaStream_t stream)
 template <int D, int BS, bool F8, bool CACHE = false>
 static cudaError_t launch_t(const AttnLaunch &a, cudaStream_t stream, const CacheTiles &ct = CacheTiles{}) {
     auto kern = sparse_attn_fwd_kernel<D, BS, F8, CACHE>;
-    // Checked once per instantiation: the number of resident CTAs per SM sizes the
-    // persistent grid.
-    static int per_sm = 0;  // 0 unknown, > 0 resident CTAs per SM, < 0 not launchable
+    // Checked once per instantiation and device (the attributes belong to the device's own copy of
+    // the function): the number of resident CTAs per SM sizes the persistent grid.
+    static std::atomic<int> known[64];  // 0 unknown, > 0 resident CTAs per SM, < 0 not launchable
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    std::atomic<int> &slot = known[dev & 63];
+    int per_sm = slot.load();
     if (per_sm == 0) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BS, F8>::SMEM_BYTES);
         if (e == cudaSuccess)
@@ -1118,6 +1124,7 @@ static cudaError_t launch_t(const AttnLaunch &a, cudaStream_t stream, const Cach
         } else {
             per_sm = occ < kCtasPerSm ? occ : kCtasPerSm;
         }
+        slot.store(per_sm);
     }
     if (per_sm < 0) return cudaErrorInvalidConfiguration;
     const int64_t cap = static_cast<int64_t>(per_sm) * a.sms;
