@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (CACHE) asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the expansion has ended
+    if (CACHE) wait_for_stream();  // launched before the expansion has ended
     const uint32_t tmem = bar->tmem_base;
     if (cta_busy_ns && threadIdx.x == 0) {
         long long t0;
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     constexpr int LANES = D / 4, GROUPS = 128 / LANES, kFewParts = 8;
     __shared__ float4 acc_s[GROUPS][LANES];
     __shared__ float l_s[GROUPS], m_s[GROUPS];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the partials are written
+    wait_for_stream();  // launched before the partials are written
     const int i = blockIdx.y;
     const int64_t total = ct.rest[ct.n_rest], u0 = ct.rest[i], u1 = ct.rest[i + 1];
     const int n = stretches(total, ct.ctas);

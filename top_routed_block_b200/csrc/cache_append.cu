@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 32 * kFewWarps : THREADS, THRE
     __shared__ RopeTable table;
     table.fill(g.a.rope);
     __syncthreads();
+    wait_for_stream();
     if (blockIdx.x == gridDim.x - 1) {
         check_append(g);
         return;
@@ -311,28 +312,31 @@ __global__ void __launch_bounds__(THREADS == 32 ? 32 * kFewWarps : THREADS, THRE
     }
 }
 
-template <int D, bool HALF, bool FULL, int THREADS, int P>
-void launch_append_ctas(const AppendArgs &g, int sms, cudaStream_t stream) {
-    const int64_t resident = static_cast<int64_t>(sms) * (1024 / THREADS) - 1;  // and the one that checks
-    const unsigned ctas = static_cast<unsigned>(g.pages < resident ? g.pages : resident) + 1;
-    cudaFuncSetAttribute(append_kernel<D, HALF, FULL, THREADS, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, P * 64 * THREADS);
-    append_kernel<D, HALF, FULL, THREADS, P><<<ctas, THREADS, P * 64 * THREADS, stream>>>(g);
+// The angles' place in shared memory: 64 bytes a thread and pass.
+template <int D, bool HALF, bool FULL, int THREADS, int PASSES>
+cudaError_t launch_append_k(const AppendArgs &g, int64_t ctas, cudaStream_t stream) {
+    constexpr int threads = THREADS == 32 ? 32 * kFewWarps : THREADS, smem = PASSES * 64 * threads;
+    const cudaError_t e = allow_shared_memory<append_kernel<D, HALF, FULL, THREADS, PASSES>>(smem);
+    if (e != cudaSuccess) return e;
+    const cudaLaunchConfig_t cfg = early_launch(dim3(static_cast<unsigned>(ctas) + 1), threads, smem, stream);  // one checks
+    return cudaLaunchKernelEx(&cfg, append_kernel<D, HALF, FULL, THREADS, PASSES>, g);
+}
+
+template <int D, bool HALF, bool FULL, int THREADS>
+cudaError_t launch_append_ctas(const AppendArgs &g, int sms, cudaStream_t stream) {
+    const int64_t resident = static_cast<int64_t>(sms) * (1024 / THREADS) - 1;
+    return launch_append_k<D, HALF, FULL, THREADS, 1>(g, g.pages < resident ? g.pages : resident, stream);
 }
 
 template <int D, bool HALF, bool FULL>
 cudaError_t launch_append_t(const AppendArgs &g, int sms, cudaStream_t stream) {
     const AppendLaunch &a = g.a;
     constexpr int covered = 512 / D;  // tokens of a warp at once
-    if (a.T <= kFewPasses * covered) {
-        const unsigned ctas = static_cast<unsigned>(ceil_div(2 * g.pages, kFewWarps)) + 1;
-        if (a.T <= covered) append_kernel<D, HALF, FULL, 32, 1><<<ctas, 32 * kFewWarps, 64 * 32 * kFewWarps, stream>>>(g);
-        else append_kernel<D, HALF, FULL, 32, kFewPasses><<<ctas, 32 * kFewWarps, kFewPasses * 64 * 32 * kFewWarps, stream>>>(g);
-    } else if (a.pool.block == 128) {
-        launch_append_ctas<D, HALF, FULL, 128 * D / 16, 1>(g, sms, stream);
-    } else {
-        launch_append_ctas<D, HALF, FULL, 64 * D / 16, 1>(g, sms, stream);
-    }
-    return cudaGetLastError();
+    const int64_t few_ctas = ceil_div(2 * g.pages, kFewWarps);
+    if (a.T <= covered) return launch_append_k<D, HALF, FULL, 32, 1>(g, few_ctas, stream);
+    if (a.T <= kFewPasses * covered) return launch_append_k<D, HALF, FULL, 32, kFewPasses>(g, few_ctas, stream);
+    return a.pool.block == 128 ? launch_append_ctas<D, HALF, FULL, 128 * D / 16>(g, sms, stream)
+                               : launch_append_ctas<D, HALF, FULL, 64 * D / 16>(g, sms, stream);
 }
 
 }  // namespace

@@ -50,7 +50,6 @@
 // tile, and one launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <atomic>
 #include <cstdint>
 #include <math_constants.h>
 
@@ -324,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
     __shared__ float4 stat_s[kWarps][kRows];
     static_assert(kRows * D * 4 <= 2 * S_::BYTES, "the sums reuse the steps' place");
     const AttendLaunch &a = g.a;
+    wait_for_stream();
     if (!g.whole) make_plan(g, first, lens);
     if (blockIdx.x == 0) {
         if (!g.whole)
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
     constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
     __shared__ float4 acc_s[GROUPS][LANES];
     __shared__ float3 stat_s[GROUPS];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the partials are still made
+    wait_for_stream();  // launched while the partials are still made
     const AttendLaunch &a = g.a;
     const int b = blockIdx.y;
     const int R = a.group * a.M;
@@ -871,20 +871,10 @@ static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
     const AttendLaunch &a = g.a;
     constexpr size_t steps = static_cast<size_t>(kWarps) * 2 * Step<D, STEP>::BYTES;
     const size_t smem = steps + (2 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-    // (the attribute belongs to the device's own copy of the function: set on its first call)
-    static std::atomic<uint64_t> ready{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = allow_shared_memory<attend_few_kernel<D, STEP>>(static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(ready.load() & bit)) {
-        e = cudaFuncSetAttribute(attend_few_kernel<D, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit);
-    }
-    attend_few_kernel<D, STEP><<<static_cast<unsigned>(g.ctas * g.row_tiles) + 1, kThreads, smem, stream>>>(g);
-    e = cudaGetLastError();
+    const cudaLaunchConfig_t work = early_launch(dim3(static_cast<unsigned>(g.ctas * g.row_tiles) + 1), kThreads, smem, stream);
+    e = cudaLaunchKernelEx(&work, attend_few_kernel<D, STEP>, g);
     if (e != cudaSuccess || g.whole) return e;
     cudaLaunchConfig_t cfg = early_launch(
         dim3(static_cast<unsigned>(a.pool.heads * attend_rows(a.group, a.M)), static_cast<unsigned>(a.B)), kJoinThreads, 0, stream);

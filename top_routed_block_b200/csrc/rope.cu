@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     __shared__ RopeTable table;
     table.fill(p);
     __syncthreads();
+    wait_for_stream();
     const int i = threadIdx.x % TPT;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / TPT) + threadIdx.x / TPT;
     if (t >= N) return;
@@ -166,18 +167,18 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const int32_t 
     const int per_group = static_cast<int>(ceil_div(heads, groups_wanted < heads ? groups_wanted : heads));
     const int groups = static_cast<int>(ceil_div(heads, per_group));
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(groups), static_cast<unsigned>(B));
+    const cudaLaunchConfig_t cfg = early_launch(grid, kRopeThreads, 0, stream);
     const bool full = 2 * p.n_pairs == d;
     const float sign = inverse ? -1.0f : 1.0f;
 #define FVATTN_ROPE(D_, H_, F_, A_) \
-    rope_kernel<D_, H_, F_, A_><<<grid, kRopeThreads, 0, stream>>>(q, k, pos, pos_b, N, per_group, sign, p)
+    cudaLaunchKernelEx(&cfg, rope_kernel<D_, H_, F_, A_>, q, k, pos, pos_b, N, per_group, sign, p)
 #define FVATTN_ROPE_F(D_, H_, A_) (full ? FVATTN_ROPE(D_, H_, true, A_) : FVATTN_ROPE(D_, H_, false, A_))
 #define FVATTN_ROPE_H(D_, A_) (half ? FVATTN_ROPE_F(D_, true, A_) : FVATTN_ROPE_F(D_, false, A_))
-    if (d == 128) is_long ? FVATTN_ROPE_H(128, kLongAhead) : FVATTN_ROPE_H(128, kShortAhead);
-    else is_long ? FVATTN_ROPE_H(64, kLongAhead) : FVATTN_ROPE_H(64, kShortAhead);
+    if (d == 128) return is_long ? FVATTN_ROPE_H(128, kLongAhead) : FVATTN_ROPE_H(128, kShortAhead);
+    return is_long ? FVATTN_ROPE_H(64, kLongAhead) : FVATTN_ROPE_H(64, kShortAhead);
 #undef FVATTN_ROPE_H
 #undef FVATTN_ROPE_F
 #undef FVATTN_ROPE
-    return cudaGetLastError();
 }
 
 }  // namespace fvattn
