@@ -266,6 +266,10 @@ def attend_case(rng, B, H, G, M, d, block, lens, new, causal, spread=3, spoil=Tr
     (2, 1, 5, 29, [129, 513], [29, 3], True),       # a tile over several heads' rows
     (3, 1, 1, 130, [128, 0, 255], [130, 0, 128], True),
     (1, 2, 1, 257, [1000], None, False),
+    (2, 3, 2, 33, [600, 2049], None, True),         # 66 rows: one tile, cut over its keys
+    (2, 2, 1, 64, [1500, 700], [64, 9], True),      # 64 rows: eight row groups
+    (1, 1, 1, 70, [512], None, True),               # a short cache: a CTA takes all of it
+    (1, 150, 1, 129, [700], None, True),            # more items than SMs: whole ones, then the rest
 ])
 def test_attend(d, block, B, H, G, M, lens, new, causal):
     attend_case(np.random.default_rng(M * 7 + d + block), B, H, G, M, d, block, lens, new, causal)
@@ -277,7 +281,7 @@ def test_attend_long_split(G, M, n):
     attend_case(np.random.default_rng(n), 1, 1, G, M, 128, 128, [n], None, True, spoil=n < 10000)
 
 
-@pytest.mark.parametrize("M", [1, 40])
+@pytest.mark.parametrize("M", [1, 40, 130])
 def test_attend_scales_far_apart(M):
     """Pages whose scales differ by 2^40, and scores in the hundreds: weights of a page with small values
     must not be lost beside those of a page with large ones that the softmax has all but removed."""
@@ -288,7 +292,7 @@ def test_attend_scales_far_apart(M):
         attend_case(rng, 2, 2, 1, M, 64, 64, [500, 300], None, False, spread=40, q_scale=q_scale, k_exp=-7)
 
 
-@pytest.mark.parametrize("M", [5, 70])
+@pytest.mark.parametrize("M", [5, 70, 150])
 def test_attend_nan_that_a_row_does_not_see(M):
     """Causal rows around a cached token with a NaN value (one channel) and a NaN key: rows before it are
     as if it were not there, rows that see the value have NaN in that channel only."""
@@ -315,7 +319,7 @@ def test_attend_nan_that_a_row_does_not_see(M):
     assert torch.isnan(O[:, :, 2:]).all() and torch.isnan(LSE[..., 2:]).all()
 
 
-@pytest.mark.parametrize("M", [2, 50])
+@pytest.mark.parametrize("M", [2, 50, 200])
 def test_attend_bad_pages(M):
     """Table entries and lengths out of range are reported, and read nothing outside the pool."""
     import top_routed_block_b200 as fv
@@ -414,6 +418,55 @@ def test_generation_run(d, block):
         step = np.repeat(2.0 ** (ke[ids].astype(float) - 10).T, block, 1)[:, :n, None]
         # one rounding when it came, and one more for each growth of a page's scale that made it subnormal
         assert (np.abs(got - said[b]) <= 2.0 ** -4 * np.abs(said[b]) + 2 * step + 1e-5).all()
+
+
+def test_attend_wide_batch():
+    """More sequences than the planning searches chunks for, most of them short or empty."""
+    rng = np.random.default_rng(61)
+    lens = [int(x) for x in rng.integers(0, 90, 70)]
+    lens[3], lens[40] = 1300, 640
+    attend_case(rng, 70, 1, 1, 1, 64, 64, lens, None, True)
+
+
+def test_append_many_items():
+    """More pages and heads than resident CTAs: stretches that end inside a page's heads."""
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(67)
+    B, H, T, d, block = 2, 23, 1300, 128, 128
+    pages, plain = random_pool(rng, 24, H, block, d)
+    table, starts = random_table(rng, 24, B, 12), [70, 129]
+    K, V = bf16(rng, B, H, T, d, layout="bnhd"), bf16(rng, B, H, T, d, layout="bnhd")
+    st = fv.fvattn_cache_append(K, V, pages, i32(table), i32(starts))
+    fv.check_status(st)
+    ref.append(plain, table, starts, [T] * B, K.double().cpu().numpy(), V.double().cpu().numpy())
+    check_pool(pages, plain)
+
+
+def test_append_on_streams_and_in_a_graph():
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(71)
+    for T in (1, 40):
+        rope, pos = fv.rope_axes((64,)), i32(np.arange(T)[:, None] + 5)
+        table, start = i32([[0, 1], [3, 2]]), i32([5, 70])
+        made = [random_pool(rng, 4, 2, 64, 64)[0] for _ in range(3)]
+        for m in made[1:]:
+            for a, b in zip(m, made[0]):
+                a.copy_(b)
+        K, V = bf16(rng, 2, 2, T, 64), bf16(rng, 2, 2, T, 64)
+        args = dict(positions=pos, rope=rope)
+        fv.check_status(fv.fvattn_cache_append(K, V, made[0], table, start, **args))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        st = fv.fvattn_cache_append(K, V, made[1], table, start, stream=s, **args)
+        s.synchronize()
+        fv.check_status(st)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            st = fv.fvattn_cache_append(K, V, made[2], table, start, **args)
+        graph.replay()
+        fv.check_status(st)
+        for a, b, c in zip(*made):
+            assert torch.equal(a, b) and torch.equal(a, c)
 
 
 def test_attend_refuses_on_the_gpu():

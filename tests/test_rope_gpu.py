@@ -1,8 +1,9 @@
 """Rotary positions with several axes on the GPU against the 64-bit formula.
 
 Bound of every element: the bf16 rounding 2^-8 |y|, and (|x_a| + |x_b|) times the error of the
-fp32 cosine and sine: the angle in half revolutions is rounded to fp32 (2^-24 of at most pi:
-1.9e-7), sincospif is good to 2 ulp (2.4e-7), the products to 2 * 2^-24 (1.2e-7): 6e-7."""
+fp32 cosine and sine: the angle from the nearest quarter turn is rounded to fp32 twice (2 * 2^-24
+of at most pi/4: 9.4e-8), the series left out come to 3e-8, its roundings to 3 * 2^-24 (1.8e-7), the
+products to 2 * 2^-24 (1.2e-7): 4.3e-7, and 6e-7 is allowed."""
 import numpy as np
 import pytest
 import torch
@@ -60,8 +61,8 @@ def test_rope(B, H, N, d, dims, layout, pairing):
 
 
 def test_rope_far_positions():
-    """Angles of positions up to 2^31: p f in fp64 is off by 2^31 2^-52 revolutions / (2 pi) each for
-    the frequency's and the product's rounding: 5e-7 more."""
+    """Angles of positions up to 2^31: the step is rounded to 2^-64 revolutions, 2^31 of which are 1e-9;
+    the extended precision of the reference is good to 2^31 2^-64 as well: far inside the 1e-6 allowed."""
     import top_routed_block_b200 as fv
     rng = np.random.default_rng(9)
     rope = fv.rope_axes((64,))

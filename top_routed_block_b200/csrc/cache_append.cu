@@ -40,12 +40,6 @@ namespace {
 constexpr int kFewWarps = 4;   // warps that own a page each, in a CTA
 constexpr int kFewPasses = 4;  // tokens such a warp takes at most, over those it covers at once
 
-__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ float2 values2(uint32_t two_codes) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two_codes)));
@@ -72,15 +66,25 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
     return r;
 }
 
-// Sixteen values times 2^-e as codes, two to a half word of q.
-__device__ __forceinline__ void codes16(const float (&v)[16], int e, uint32_t (&q)[8]) {
+// Four values -> four codes, the first in the low byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{.reg .b16 lo, hi; cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1; cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3; mov.b32 %0, {lo, hi};}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// Sixteen values times 2^-e as codes.
+__device__ __forceinline__ void codes16(const float (&v)[16], int e, uint32_t (&q)[4]) {
     if (e >= -127 && e <= 126) {  // 2^-e is a normal number
         const float f = __int_as_float((127 - e) << 23);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = codes2(v[2 * k] * f, v[2 * k + 1] * f);
+        for (int k = 0; k < 4; ++k) q[k] = codes4(v[4 * k] * f, v[4 * k + 1] * f, v[4 * k + 2] * f, v[4 * k + 3] * f);
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = codes2(scale_pow2(v[2 * k], -e), scale_pow2(v[2 * k + 1], -e));
+        for (int k = 0; k < 4; ++k)
+            q[k] = codes4(scale_pow2(v[4 * k], -e), scale_pow2(v[4 * k + 1], -e), scale_pow2(v[4 * k + 2], -e),
+                          scale_pow2(v[4 * k + 3], -e));
     }
 }
 
@@ -88,6 +92,7 @@ struct AppendArgs {
     AppendLaunch a;
     int touched;    // pages a sequence's new tokens can touch
     int64_t pages;  // (sequence, touched page, head), in this order
+    bool apart;     // K and V of one of them to a warp, or a CTA, each
 };
 
 __device__ void check_append(const AppendArgs &g) {
@@ -117,7 +122,6 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
     constexpr int TPT = D / 16;          // threads of a token: two vectors of 8 channels each
     constexpr int TOKS = THREADS / TPT;  // tokens a pass covers
     constexpr int WARPS = THREADS / 32;
-    constexpr bool PREFETCH = true;
     const AppendLaunch &a = g.a;
     const int tid = static_cast<int>(threadIdx.x) % THREADS;
     const int H = a.pool.heads, BS = a.pool.block;
@@ -177,7 +181,6 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
         auto load = [&](int ahead) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                ra[p] = rb[p] = make_uint4(0, 0, 0, 0);
                 if (slot0 + p * TOKS < sp.hi) {
                     ra[p] = __ldg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + ca));
                     rb[p] = __ldg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + cb));
@@ -210,8 +213,10 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
         for (int h = h0; h < h1; ++h) {
             const int e_old = clamp_exp(e_next);
             float y[PASSES][16];
+            float amax = 0.0f;
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
+                if (slot0 + p * TOKS >= sp.hi) continue;
                 const uint32_t w[8] = {ra[p].x, ra[p].y, ra[p].z, ra[p].w, rb[p].x, rb[p].y, rb[p].z, rb[p].w};
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -219,11 +224,11 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
                     y[p][2 * q + 1] = rope_bf16_hi(w[q]);
                 }
             }
-            if (PREFETCH && h + 1 < h1) load(1);
-            if (turn) {
+            if (h + 1 < h1) load(1);
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p) {
-                    if (slot0 + p * TOKS >= sp.hi) continue;
+            for (int p = 0; p < PASSES; ++p) {
+                if (slot0 + p * TOKS >= sp.hi) continue;
+                if (turn) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const float4 cs = mine[(p * 4 + q / 2) * stride];
@@ -237,12 +242,9 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
                         }
                     }
                 }
-            }
-            float amax = 0.0f;
-#pragma unroll
-            for (int p = 0; p < PASSES; ++p)
 #pragma unroll
                 for (int q = 0; q < 16; q += 2) amax = max_abs(amax, y[p][q], y[p][q + 1]);
+            }
             // (numbers that are not negative order as their bits do)
             amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
             if constexpr (WARPS > 1) {
@@ -263,8 +265,8 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const float2 x0 = values2(o4[w] & 0xffffu), x1 = values2(o4[w] >> 16);
-                        o4[w] = codes2(scale_pow2(x0.x, shift), scale_pow2(x0.y, shift)) |
-                                (codes2(scale_pow2(x1.x, shift), scale_pow2(x1.y, shift)) << 16);
+                        o4[w] = codes4(scale_pow2(x0.x, shift), scale_pow2(x0.y, shift), scale_pow2(x1.x, shift),
+                                       scale_pow2(x1.y, shift));
                     }
                     old[q] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
                 }
@@ -273,13 +275,12 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
             for (int p = 0; p < PASSES; ++p) {
                 const int slot = slot0 + p * TOKS;
                 if (slot >= sp.hi) continue;
-                uint32_t q[8];
+                uint32_t q[4];
                 codes16(y[p], e, q);
                 uint8_t *row = codes + slot * D;
-                *reinterpret_cast<uint2 *>(row + ca) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-                *reinterpret_cast<uint2 *>(row + cb) = make_uint2(q[4] | (q[5] << 16), q[6] | (q[7] << 16));
+                *reinterpret_cast<uint2 *>(row + ca) = make_uint2(q[0], q[1]);
+                *reinterpret_cast<uint2 *>(row + cb) = make_uint2(q[2], q[3]);
             }
-            if (!PREFETCH && h + 1 < h1) load(1);
             codes += BS * D;
             ++exps;
         }
@@ -299,12 +300,12 @@ __global__ void __launch_bounds__(THREADS == 32 ? 32 * kFewWarps : THREADS, THRE
         return;
     }
     int barriers = 0;
-    if (THREADS == 32) {  // a warp takes K or V of one item
-        const int64_t x = static_cast<int64_t>(blockIdx.x) * kFewWarps + threadIdx.x / 32, item = x >> 1;
-        const int64_t end = min(item + 1, g.pages);
+    if (THREADS == 32 || g.apart) {
+        const int64_t x = THREADS == 32 ? static_cast<int64_t>(blockIdx.x) * kFewWarps + threadIdx.x / 32 : blockIdx.x;
+        const int64_t item = x >> 1, end = min(item + 1, g.pages);
         if (x & 1) append_items<D, HALF, FULL, THREADS, PASSES, false>(g, item, end, table, warp_max, barriers);
         else append_items<D, HALF, FULL, THREADS, PASSES, true>(g, item, end, table, warp_max, barriers);
-    } else {  // a CTA takes both of a stretch of them
+    } else {  // K, then V, of a stretch of them
         const int64_t item = stretch_start(blockIdx.x, g.pages, gridDim.x - 1);
         const int64_t end = stretch_start(blockIdx.x + 1, g.pages, gridDim.x - 1);
         append_items<D, HALF, FULL, THREADS, PASSES, true>(g, item, end, table, warp_max, barriers);
@@ -323,9 +324,11 @@ cudaError_t launch_append_k(const AppendArgs &g, int64_t ctas, cudaStream_t stre
 }
 
 template <int D, bool HALF, bool FULL, int THREADS>
-cudaError_t launch_append_ctas(const AppendArgs &g, int sms, cudaStream_t stream) {
+cudaError_t launch_append_ctas(AppendArgs g, int sms, cudaStream_t stream) {
     const int64_t resident = static_cast<int64_t>(sms) * (1024 / THREADS) - 1;
-    return launch_append_k<D, HALF, FULL, THREADS, 1>(g, g.pages < resident ? g.pages : resident, stream);
+    g.apart = 2 * g.pages <= resident;
+    const int64_t ctas = g.apart ? 2 * g.pages : g.pages < resident ? g.pages : resident;
+    return launch_append_k<D, HALF, FULL, THREADS, 1>(g, ctas, stream);
 }
 
 template <int D, bool HALF, bool FULL>
@@ -343,7 +346,7 @@ cudaError_t launch_append_t(const AppendArgs &g, int sms, cudaStream_t stream) {
 
 cudaError_t launch_cache_append(const AppendLaunch &a, int sms, cudaStream_t stream) {
     const int64_t touched = max_touched_pages(a.T, a.pool.block);
-    const AppendArgs g{a, static_cast<int>(touched), a.B * touched * a.pool.heads};
+    const AppendArgs g{a, static_cast<int>(touched), a.B * touched * a.pool.heads, true};
     const bool full = !a.pos || 2 * a.rope.n_pairs == a.pool.d;  // every channel turns
 #define FVATTN_APPEND(D_) \
     (a.half ? full ? launch_append_t<D_, true, true>(g, sms, stream) : launch_append_t<D_, true, false>(g, sms, stream) \
