@@ -859,10 +859,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             dst[q] = make_uint4(pkk[4 * q], pkk[4 * q + 1], pkk[4 * q + 2], pkk[4 * q + 3]);
                     }
                 }
-                if (row_ok && CACHE && partial) {
-                } else if (row_ok && CACHE)  // a NaN sum stays one
+                if (CACHE && row_ok && !partial)  // a NaN sum stays one
                     LSE[crow.lse_at] = (l == 0.0f) ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
-                else if (row_ok)
+                if (!CACHE && row_ok)
                     LSE[bh * N + t_row] = (l > 0.0f) ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
                 tc_fence_before();
                 __syncwarp();

@@ -109,8 +109,8 @@ __device__ __forceinline__ void check_attend(const AttendLaunch &a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // four entries' loads at a time
             const int i = i0 + k * stride;
-            page[k] = i < all ? __ldg(a.pool.table + i) : 0;
-            len[k] = i < all ? __ldg(a.lens + i / a.pool.max_pages) : 0;
+            page[k] = i < all ? __ldcg(a.pool.table + i) : 0;
+            len[k] = i < all ? __ldcg(a.lens + i / a.pool.max_pages) : 0;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

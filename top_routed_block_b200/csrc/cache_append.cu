@@ -182,8 +182,8 @@ __device__ __forceinline__ void append_items(const AppendArgs &g, int64_t item, 
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
                 if (slot0 + p * TOKS < sp.hi) {
-                    ra[p] = __ldg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + ca));
-                    rb[p] = __ldg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + cb));
+                    ra[p] = __ldcg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + ca));
+                    rb[p] = __ldcg(reinterpret_cast<const uint4 *>(from + p * TOKS * src_n + cb));
                 }
             }
             from += src_h;

@@ -167,7 +167,7 @@ __device__ void make_plan(const FewArgs &g, int *first, int *lens) {
         const int groups = a.pool.heads;
         int total = 0;
         for (int b = lane; b < a.B; b += 32) {
-            lens[b] = static_cast<int>(clamp_len(a.lens[b], cap));
+            lens[b] = sequence(a, b).n_new > 0 ? static_cast<int>(clamp_len(a.lens[b], cap)) : 0;  // (nothing to write)
             total += units_of(g, lens[b]) * groups;
         }
         total = __reduce_add_sync(0xffffffffu, total);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             unit = unit_end;
         } else {
             b = find_sequence(first, a.B, unit);
-            seq = Seq{lens[b], a.new_lens ? static_cast<int>(clamp_len(__ldg(a.new_lens + b), a.M)) : a.M};
+            seq = Seq{lens[b], a.new_lens ? static_cast<int>(clamp_len(a.new_lens[b], a.M)) : a.M};
             all = units_of(g, seq.len);
             const int at = unit - first[b];
             if (chunk) {  // its chunks are as even as can be
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
         // the page and head of the step at `tok`, or -1: behind the end, or an entry outside the pool
         auto page_at = [&](int tok) -> int64_t {
             if (tok >= c1) return -1;
-            const int p = checked_page(__ldg(table + (tok >> g.log2_block)), a.pool.num_pages);
+            const int p = checked_page(table[tok >> g.log2_block], a.pool.num_pages);
             return p < 0 ? -1 : static_cast<int64_t>(p) * H + h;
         };
         // this warp's step at tok is on its way (copy groups K, V); the page of the next is looked up
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             const int64_t at = (ph * BS + (tok & (BS - 1))) * D + lane * 16;
             if (ph >= 0) {
                 S_::copy(k_at, a.pool.k + at, copy_place);
-                ek = __ldg(a.pool.ke + ph);
-                ev = __ldg(a.pool.ve + ph);
+                ek = a.pool.ke[ph];
+                ev = a.pool.ve[ph];
             }
             copies_commit();
             if (ph >= 0) S_::copy(v_at, a.pool.v + at, copy_place);
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
                 for (int w2 = 0; w2 < 2; ++w2) {
-                    const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(qr + c * 64 + lq * 16 + w2 * 8))
+                    const uint4 v = in ? *reinterpret_cast<const uint4 *>(qr + c * 64 + lq * 16 + w2 * 8)
                                        : make_uint4(0, 0, 0, 0);
                     raw[c * 4 + w2 * 2][0] = v.x;
                     raw[c * 4 + w2 * 2][1] = v.y;
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             const int ek_here = clamp_exp(ek);
             const float evf = static_cast<float>(clamp_exp(ev));
             if (more) {
-                ek = __ldg(a.pool.ke + ph_next);
-                ev = __ldg(a.pool.ve + ph_next);
+                ek = a.pool.ke[ph_next];
+                ev = a.pool.ve[ph_next];
             }
             ph = ph_next;
             ph_next = page_at(tok + 2 * UNIT);

@@ -36,7 +36,9 @@ struct Carver {
 
 // A launch that may begin before the kernel in front of it in the stream has ended: the kernel waits for
 // that one itself (wait_for_stream) before it reads or writes anything, so that only the launch is
-// overlapped.  It saves about 1 us a call where calls for single tokens follow each other.
+// overlapped.  It saves about 1 us a call where calls for single tokens follow each other.  What the
+// kernel in front may have written is not read through the read-only path (__ldg): that is for data
+// that nobody writes while the kernel lives, and this one lives already.
 inline cudaLaunchConfig_t early_launch(dim3 grid, unsigned threads, size_t smem, cudaStream_t stream) {
     static cudaLaunchAttribute early = [] {
         cudaLaunchAttribute a{};

@@ -101,7 +101,7 @@ __device__ __forceinline__ void walk_heads(const RopeTensor &x, int h0, int h1, 
 template <int D, bool HALF, bool FULL, int AHEAD>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeTensor q, const __grid_constant__ RopeTensor k,
-                const int32_t *__restrict__ pos, int64_t pos_b, int N, int heads_per_group, float sign,
+                const int32_t *pos, int64_t pos_b, int N, int heads_per_group, float sign,
                 const __grid_constant__ RopeParams p) {
     constexpr int TPT = D / 16;  // threads of a token
     __shared__ RopeTable table;

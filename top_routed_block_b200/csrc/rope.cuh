@@ -82,7 +82,7 @@ struct RopePos {
 __device__ __forceinline__ RopePos rope_load_pos(const int32_t *p, int n_axes) {
     RopePos r;
 #pragma unroll
-    for (int a = 0; a < kMaxRopeAxes; ++a) r.x[a] = a < n_axes ? __ldg(p + a) : 0;
+    for (int a = 0; a < kMaxRopeAxes; ++a) r.x[a] = a < n_axes ? p[a] : 0;
     return r;
 }
 
