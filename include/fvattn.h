@@ -533,7 +533,7 @@ FVATTN_API size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int grou
  * fvattn_cache_attend -- exact attention of each sequence's M newest tokens over its
  * cached keys and values (FlashAttention review §Model: one pass, running maximum and sum).
  *   Q, O          device bf16 [B, heads * group, M, d], strides as fvattn_rope's (O's rows must
- *                 not overlap); query head h reads key head h / group.
+ *                 not overlap, nor O's and Q's); query head h reads key head h / group.
  *   lens          device int32 [B]: cached tokens, the new ones among them (after the append).
  *   new_lens      device int32 [B], 0 .. M query tokens of each sequence, or null: M for all.
  *                 Rows behind them are neither read nor written in O and LSE.
@@ -547,8 +547,8 @@ FVATTN_API size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int grou
  * fvattn_sparse_fwd.  Both sum in fp32.  The result does not depend on what else runs; no atomics
  * on floating values.  Exponents outside [-250, 250] are taken as the nearer end.
  * *dev_status (written by the call): FVATTN_ERR_BAD_PAGE where lens is outside [0, max_pages *
- * block], new_lens outside [0, M] (both are clamped), or an entry of the page table in use is
- * outside [0, num_pages) (with many rows its tokens count as zeros, with few they are left out: the
+ * block], new_lens outside [0, M] (both are clamped), or a page table entry of a sequence's cached
+ * tokens, where the sequence has queries, is outside [0, num_pages) (with many rows its tokens count as zeros, with few they are left out: the
  * result is not to be used); FVATTN_ERR_DEVICE_TIMEOUT as fvattn_sparse_fwd.
  * B <= 4096; B * heads * max_pages * block / 64 < 2^31; group * M < 2^24.
  */

@@ -113,6 +113,7 @@ def attend_args(**kw):
     (dict(group=0), INVALID), (dict(causal=2), INVALID), (dict(d=96), UNSUPPORTED), (dict(block=32), UNSUPPORTED),
     (dict(B=4097), UNSUPPORTED), (dict(max_pages=1 << 25), UNSUPPORTED), (dict(O=P(24)), ALIGNMENT),
     (dict(Q=P(24)), ALIGNMENT), (dict(qs=strides(0, 3, 64)), ALIGNMENT), (dict(os=strides(0, 0, 64)), INVALID),
+    (dict(O=FAKE), INVALID),   # where Q lies
     (dict(ws_bytes=64), CAPACITY), (dict(M=100, ws_bytes=64, os=strides(0, 6400, 64)), CAPACITY),
 ])
 def test_attend_refuses(lib, change, rc):

@@ -337,6 +337,30 @@ def test_attend_bad_pages(M):
     fv.check_status(st)
 
 
+@pytest.mark.parametrize("M", [1, 9, 70])
+@pytest.mark.parametrize("B", [3, 70])   # the work of few rows in chunks, in stretches
+def test_attend_bad_pages_of_long_tables(B, M):
+    """A bad entry anywhere among a sequence's cached tokens is reported, one behind them or of a sequence
+    without queries is not; the next good call says so."""
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(42)
+    pages, _ = random_pool(rng, 12, 2, 64, 64)
+    Q = bf16(rng, B, 2, M, 64)
+    good = rng.integers(0, 12, (B, 11)).astype(np.int32)
+    lens = rng.integers(M, 500, B).astype(np.int32)
+    lens[1], lens[2] = 11 * 64 - 5, 300
+    new = np.full(B, M, np.int32)
+    new[2] = 0
+    status = torch.empty(1, dtype=torch.int32, device="cuda")
+    for (b, pg), bad in [((1, 0), True), ((1, 6), True), ((1, 10), True), ((2, 1), False), ((0, 10), False), ((0, 0), True)]:
+        table = good.copy()
+        table[b, pg] = 12 if pg else -1
+        fv.fvattn_cache_attend(Q, pages, i32(table), i32(lens), new_lens=i32(new), dev_status=status)
+        assert int(status) == (fv.FVATTN_ERR_BAD_PAGE if bad else 0), (b, pg)
+    fv.fvattn_cache_attend(Q, pages, i32(good), i32(lens), new_lens=i32(new), dev_status=status)
+    assert int(status) == 0
+
+
 @pytest.mark.parametrize("M", [1, 3, 65])
 def test_attend_repeats_streams_graphs(M):
     """The same bits again, on another stream, two calls at once, and captured and replayed with other

@@ -128,6 +128,19 @@ def test_rope_on_another_stream_and_in_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+def test_rope_angles_that_vanish_or_turn_backwards():
+    """A step just below zero revolutions is none (not one short of a whole); negative frequencies turn back."""
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(15)
+    pos = torch.arange(40, dtype=torch.int32, device="cuda").view(40, 1)
+    Q, _ = make(rng, 1, 2, 40, 64, "bhnd")
+    axis = np.zeros(32, np.int32)
+    still = fv.RopeAxes(np.full(32, -1e-30), axis)
+    assert torch.equal(fv.fvattn_rope(Q, None, pos, still)[0], Q)
+    back = fv.RopeAxes(-fv.rope_axes((64,)).inv_freq, axis)
+    check(fv.fvattn_rope(Q, None, pos, back)[0], Q, pos, back)
+
+
 def test_rope_refuses_on_the_gpu():
     import top_routed_block_b200 as fv
     Q = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16, device="cuda")
@@ -143,6 +156,10 @@ def test_rope_refuses_on_the_gpu():
         fv.fvattn_rope(Q, None, pos, rope._replace(pairing="neither"))
     with pytest.raises(ValueError):
         fv.fvattn_rope(Q, Q[:, :, :4], pos, rope)
+    with pytest.raises(fv.FvattnError):   # an axis that is 0 only in 32 bits
+        fv.fvattn_rope(Q, None, pos, rope._replace(pair_axis=[1 << 32] * 32))
+    with pytest.raises(RuntimeError):     # no single truth value
+        fv.fvattn_rope(Q, None, pos, rope, inverse=pos)
     with pytest.raises(fv.FvattnError):
         fv.fvattn_rope(Q, None, pos, rope, out_q=Q[:, :1].expand(1, 2, 8, 64))
 
@@ -162,9 +179,12 @@ def test_training_step_with_positions():
     plan = fv.FvattnPlan(B, H, N, d, 128)
     O, LSE, st = plan(Q, K, Vc, 1.0, positions=pos, rope=rope)
     plan.check()
+    turned = plan.turned
     dO = torch.randn(B, H, N, d, device="cuda").to(torch.bfloat16)
     gq, gk, gv, st = fv.fvattn_sparse_bwd(*plan.turned, Vc, O, LSE, dO, plan.route.row_ptr, plan.route.col_idx, 128)
     fv.check_status(st)
+    plan(*turned, Vc, 1.0)
+    assert plan.turned is None   # of the last call, which turned nothing
     grad = torch.empty_like(x)
     fv.fvattn_rope_bwd(gq, gk, pos, rope, out_q=grad[:, :, 0].transpose(1, 2), out_k=grad[:, :, 1].transpose(1, 2))
     grad[:, :, 2] = gv.transpose(1, 2)

@@ -600,6 +600,7 @@ class FvattnPlan:
         first and stay in ``turned``, which is what fvattn_sparse_bwd takes."""
         if (positions is None) != (rope is None):
             raise ValueError("positions and rope belong together")
+        self.turned = None
         if rope is not None:
             self.turned = Q, K = fvattn_rope(Q, K, positions, rope, stream=stream)
         self.run_route(Q, K, p, stream=stream)

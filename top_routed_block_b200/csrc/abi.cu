@@ -228,7 +228,8 @@ int make_rope(RopeParams *p, const double *inv_freq, const int32_t *pair_axis, i
         if (!std::isfinite(inv_freq[j]) || pair_axis[j] < 0 || pair_axis[j] >= n_axes) return FVATTN_ERR_INVALID_ARG;
         // modulo one revolution, in 2^-64 of it (long double: 64 bits)
         const long double turns = inv_freq[j] / 6.283185307179586476925286766559L;
-        p->step[j] = static_cast<uint64_t>((turns - std::floor(turns)) * 18446744073709551616.0L);
+        const long double part = turns - std::floor(turns);  // (1 where turns is just below 0)
+        p->step[j] = part < 1.0L ? static_cast<uint64_t>(part * 18446744073709551616.0L) : 0;
         p->axis[j] = static_cast<uint8_t>(pair_axis[j]);
     }
     p->n_pairs = n_pairs;
@@ -919,7 +920,7 @@ int fvattn_cache_append(const void *K, const int64_t *k_strides, const void *V, 
 
 size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int group, int M, int d, int block, int max_pages) {
     if (check_attend_shape(B, heads, group, M, d, block, max_pages) != FVATTN_OK) return 0;
-    if (attend_few_rows(group, M, static_cast<int64_t>(max_pages) * block)) return attend_few_workspace(B, d, kPlanSms);
+    if (attend_few_rows(group, M, static_cast<int64_t>(max_pages) * block)) return attend_few_workspace(d, kPlanSms);
     return cache_tiles_layout(static_cast<int64_t>(B) * heads, d, block, max_pages).total;
 }
 
@@ -942,6 +943,7 @@ int fvattn_cache_attend(const void *Q, const int64_t *q_strides, int B, int head
     if ((rc = check_out_strides(o_strides, B, static_cast<int64_t>(heads) * group, M, d)) != FVATTN_OK) return rc;
     if (ws_bytes < fvattn_cache_attend_workspace_bytes(B, heads, group, M, d, block, max_pages))
         return FVATTN_ERR_CAPACITY;
+    if (O == Q) return FVATTN_ERR_INVALID_ARG;  // a row's other CTAs may still read its query
     DeviceInfo info;
     if ((rc = check_device()) != FVATTN_OK) return rc;
     if (!device_info(&info)) return FVATTN_ERR_CUDA;

@@ -118,7 +118,10 @@ Pairs pairs_of(PyObject *rope) {
     const int64_t n = read_list(PyTuple_GET_ITEM(rope, 0), p.freq, 'd', "inv_freq is a list of numbers",
                                 [](PyObject *x) { return PyFloat_AsDouble(x); });
     const int64_t m = read_list(PyTuple_GET_ITEM(rope, 1), p.axis, 'i', "pair_axis is a list of whole numbers",
-                                [](PyObject *x) { return static_cast<int32_t>(PyLong_AsLong(x)); });
+                                [](PyObject *x) {
+                                    const long i = PyLong_AsLong(x);
+                                    return i == static_cast<int32_t>(i) ? static_cast<int32_t>(i) : -1;  // (-1 is refused)
+                                });
     if (n != m || n > 1 << 20) refuse("rope", "inv_freq and pair_axis are two lists of the same length");
     p.n = static_cast<int>(n);
     PyObject *name = PyTuple_GET_ITEM(rope, 2);
@@ -219,6 +222,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Positions pos = positions_of(a[2], q.size[0], q.size[2], q.device);
         const Pairs p = pairs_of(a[3]);
         const int inverse = PyObject_IsTrue(a[4]);
+        if (inverse < 0) return nullptr;
         const c10::cuda::CUDAGuard guard(q.device);
         auto out = [&](PyObject *given, const Heads &like, const char *what) {
             at::Tensor t = given != Py_None ? tensor(given, what)
@@ -291,6 +295,7 @@ PyObject *cache_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int32_t *lens = int32_of(tensor(a[3], "lens"), {B}, q.device, "lens");
         const int32_t *new_lens = a[4] == Py_None ? nullptr : int32_of(tensor(a[4], "new_lens"), {B}, q.device, "new_lens");
         const int causal = PyObject_IsTrue(a[5]);
+        if (causal < 0) return nullptr;
         const c10::cuda::CUDAGuard guard(q.device);
         const at::Tensor O = a[6] == Py_None ? empty({B, Hq, M, q.size[3]}, at::kBFloat16, q.device) : tensor(a[6], "O");
         const Heads o = heads_of(O, "O");

@@ -58,7 +58,7 @@ inline int64_t attend_rows(int group, int M) { return static_cast<int64_t>(group
 // Whether the call takes the few-rows kernel (else the pages are expanded and the tensor
 // cores' 128-row tiles run over them).
 bool attend_few_rows(int group, int M, int64_t capacity);
-size_t attend_few_workspace(int B, int d, int sms);
+size_t attend_few_workspace(int d, int sms);
 cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream);
 #ifdef __CUDACC__
 
@@ -94,7 +94,9 @@ __device__ __forceinline__ int row_limit(const AttendLaunch &a, const Seq &s, in
     return a.causal ? static_cast<int>(clamp_len(static_cast<int64_t>(s.len) - s.n_new + m + 1, s.len)) : s.len;
 }
 
-// Lengths, counts and the page table entries in use; one CTA, writes the status word.
+// Lengths, counts and (TABLE) the page table entries in use: those of sequences with queries.  One CTA,
+// writes the status word.
+template <bool TABLE>
 __device__ __forceinline__ void check_attend(const AttendLaunch &a) {
     const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
     bool bad = false;
@@ -102,20 +104,21 @@ __device__ __forceinline__ void check_attend(const AttendLaunch &a) {
         const int64_t len = a.lens[b], n = a.new_lens ? a.new_lens[b] : a.M;
         if (len < 0 || len > cap || n < 0 || n > a.M) bad = true;
     }
-    const int all = a.B * a.pool.max_pages, stride = static_cast<int>(blockDim.x);
+    const int all = TABLE ? a.B * a.pool.max_pages : 0, stride = static_cast<int>(blockDim.x);
     for (int i0 = threadIdx.x; i0 < all; i0 += 4 * stride) {
         int page[4];
-        int64_t len[4];
+        int used[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // four entries' loads at a time
             const int i = i0 + k * stride;
             page[k] = i < all ? __ldcg(a.pool.table + i) : 0;
-            len[k] = i < all ? __ldcg(a.lens + i / a.pool.max_pages) : 0;
+            const Seq seq = i < all ? sequence(a, i / a.pool.max_pages) : Seq{0, 0};
+            used[k] = seq.n_new > 0 ? seq.len : 0;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int i = i0 + k * stride;
-            if (i < all && static_cast<int64_t>(i % a.pool.max_pages) * a.pool.block < clamp_len(len[k], cap) &&
+            if (i < all && static_cast<int64_t>(i % a.pool.max_pages) * a.pool.block < used[k] &&
                 checked_page(page[k], a.pool.num_pages) < 0)
                 bad = true;
         }

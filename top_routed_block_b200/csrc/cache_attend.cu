@@ -72,18 +72,19 @@ constexpr int kWholeTokens = 512;       // caches this short: a CTA takes a whol
 constexpr int kCtasPerSm = 3;           // by shared memory (64 KB each at d 128) and registers
 constexpr int kChunkShare = 8;          // units per CTA below which segments are cut into chunks
 constexpr int kChunkSequences = 64;     // more sequences are not worth the search for the chunk
+constexpr int kMostCtas = 512;          // stretches (444 CTAs are resident on 148 SMs)
 constexpr int kJoinThreads = 128;
 constexpr float kWeightLog2 = 15.0f;    // weights are scaled by 2^15 before fp16
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct FewWorkspace {
-    size_t plan, stats, acc, total;
+    size_t split, stats, acc, total;
 };
 
-FewWorkspace few_layout(int B, int d, int ctas) {
+FewWorkspace few_layout(int d, int ctas) {
     FewWorkspace w{};
     Carver c;
-    w.plan = c.take<int32_t>(static_cast<size_t>(B) + 2);
+    w.split = c.take<int4>(static_cast<size_t>(ctas));
     w.stats = c.take<float4>(static_cast<size_t>(ctas) * 2 * kRows);
     w.acc = c.take<float>(static_cast<size_t>(ctas) * 2 * kRows * d);
     w.total = align_up(c.off, 256);
@@ -92,7 +93,8 @@ FewWorkspace few_layout(int B, int d, int ctas) {
 
 struct FewArgs {
     AttendLaunch a;
-    int32_t *plan;    // [B + 2] the plan, from CTA 0 for the joining kernel
+    int4 *split;      // [ctas] the segment that begins in a stretch and ends behind it: sequence, key head,
+                      // parts (0: none); and whether the stretch met a bad page table entry
     int unit;         // tokens
     float4 *stats;    // [2 * ctas, kRows]: m, l, w
     float *acc;       // [2 * ctas, kRows, d]
@@ -158,20 +160,20 @@ __device__ __forceinline__ int units_of(const FewArgs &g, int len) {
 
 // The plan, in shared memory: first[b] = what comes before sequence b, for b = 0 .. B, in units
 // (stretches) or in chunks of at most first[B + 1] units; first[B + 1] = 0 says stretches.
-// Every CTA makes the same plan in its shared memory: one warp, the others wait.
+// Every CTA makes the same plan in its shared memory: all load the lengths, one warp adds.
 __device__ void make_plan(const FewArgs &g, int *first, int *lens) {
     const AttendLaunch &a = g.a;
-    const int64_t cap = static_cast<int64_t>(a.pool.max_pages) * a.pool.block;
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+        const Seq seq = sequence(a, b);
+        lens[b] = seq.n_new > 0 ? seq.len : 0;  // (nothing to write)
+    }
+    __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         const int groups = a.pool.heads;
         int total = 0;
-        for (int b = lane; b < a.B; b += 32) {
-            lens[b] = sequence(a, b).n_new > 0 ? static_cast<int>(clamp_len(a.lens[b], cap)) : 0;  // (nothing to write)
-            total += units_of(g, lens[b]) * groups;
-        }
+        for (int b = lane; b < a.B; b += 32) total += units_of(g, lens[b]) * groups;
         total = __reduce_add_sync(0xffffffffu, total);
-        __syncwarp();
         // the smallest chunk, of 1 .. 32 units, with which every chunk gets its own CTA
         int chunk = 0;
         if (total < kChunkShare * g.ctas && a.B <= kChunkSequences) {
@@ -315,20 +317,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
     constexpr int ST = STEP / 16;   // 16-token tiles of a step
     constexpr int UNIT = STEP * kWarps;
     using S_ = Step<D, STEP>;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];  // whole lines (16 bytes off: 142 -> 159 us)
     unsigned char *kr = smem + (threadIdx.x >> 5) * 2 * S_::BYTES, *vr = kr + S_::BYTES;  // this warp's K and V
     float *acc_s = reinterpret_cast<float *>(smem);  // [kWarps][kRows][D], between segments
     int *first = reinterpret_cast<int *>(smem + kWarps * 2 * S_::BYTES);
     int *lens = first + g.a.B + 2;
     __shared__ float4 stat_s[kWarps][kRows];
+    __shared__ int4 split_s;
     static_assert(kRows * D * 4 <= 2 * S_::BYTES, "the sums reuse the steps' place");
     const AttendLaunch &a = g.a;
     wait_for_stream();
-    if (!g.whole) make_plan(g, first, lens);
-    if (blockIdx.x == 0) {
-        if (!g.whole)
-            for (int i = threadIdx.x; i < a.B + 2; i += kThreads) g.plan[i] = first[i];
-        check_attend(a);
+    if (threadIdx.x == 0) split_s = make_int4(0, 0, 0, 0);
+    if (!g.whole && blockIdx.x > 0) make_plan(g, first, lens);
+    if (blockIdx.x == 0) {  // (with a plan, the others check the table's entries as they meet them)
+        if (g.whole) check_attend<true>(a);
+        else check_attend<false>(a);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -346,8 +349,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
         const int total = first[a.B];
         chunk = first[a.B + 1];
         const int n = stretches(total, g.ctas);
-        if (stretch >= n) return;
-        if (!chunk) {
+        if (stretch >= n) {
+            unit_end = unit;  // nothing left for it
+        } else if (!chunk) {
             unit = static_cast<int>(stretch_start(stretch, total, n));
             unit_end = static_cast<int>(stretch_start(stretch + 1, total, n));
         }
@@ -373,11 +377,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
                 off = static_cast<int>(stretch_start(at % n, all, n));
                 n_units = static_cast<int>(stretch_start(at % n + 1, all, n)) - off;
                 unit = unit_end;
+                if (off == 0 && threadIdx.x == 0) split_s.x = b, split_s.y = h, split_s.z = n;
             } else {
                 h = at / all;
                 off = at % all;
                 n_units = min(all - off, unit_end - unit);
                 unit += n_units;
+                if (off == 0 && n_units < all && threadIdx.x == 0) {
+                    const int total = first[a.B], last = first[b] + (h + 1) * all - 1;
+                    split_s.x = b, split_s.y = h;
+                    split_s.z = stretch_of(last, total, stretches(total, g.ctas)) - stretch + 1;
+                }
             }
         }
 
@@ -494,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             ph_next = page_at(tok + 2 * UNIT);
             copies_wait<1>();  // K of this step
             if (!here) {       // an entry outside the pool: its tokens are left out
+                split_s.w = 1;
                 copies_wait<0>();
                 if (more) S_::copy(k_at, a.pool.k + at_next, copy_place);
                 copies_commit();
@@ -689,52 +700,45 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
         }
         __syncthreads();
     }
+    if (!g.whole && rt == 0 && threadIdx.x == 0) g.split[stretch] = split_s;
 }
 
-// Joins the partials of one row: grid (key head and row, sequence).  They go to the CTA's groups
-// of D / 4 threads in turn, and the groups are added in order.
+// Joins the partials of one row: grid (row, stretch), of the segment that begins in the stretch and goes on
+// behind it.  They go to the CTA's groups of D / 4 threads in turn, and the groups are added in order.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ FewArgs g) {
     constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
+    __shared__ float4 part_s[kMostCtas];
     __shared__ float4 acc_s[GROUPS][LANES];
     __shared__ float3 stat_s[GROUPS];
     wait_for_stream();  // launched while the partials are still made
     const AttendLaunch &a = g.a;
-    const int b = blockIdx.y;
-    const int R = a.group * a.M;
-    const int h = blockIdx.x / R, r = blockIdx.x % R;
-    const Seq seq = sequence(a, b);
-    if (r % a.M >= seq.n_new) return;
-    const int total = g.plan[a.B], before = g.plan[b], chunk = g.plan[a.B + 1], units = units_of(g, seq.len);
-    const int rt = r / kRows;
-    // stretches from..: a segment's first part is the second partial of its CTA (of the segment that CTA
-    // ends in), the others are the first of theirs
-    int from, n_parts;
-    if (chunk) {
-        n_parts = (units + chunk - 1) / chunk;
-        from = before + h * n_parts;
-    } else {
-        const int n = stretches(total, g.ctas);
-        const int64_t u0 = before + static_cast<int64_t>(h) * units;
-        from = stretch_of(u0, total, n);
-        n_parts = stretch_of(u0 + units - 1, total, n) - from + 1;
+    const int r = blockIdx.x, from = blockIdx.y;
+    if (r == 0 && from == 0) {
+        bool bad = false;
+        for (int i = threadIdx.x; i < g.ctas; i += kJoinThreads) bad |= g.split[i].w != 0;
+        if (bad) *a.dev_status = FVATTN_ERR_BAD_PAGE;
     }
-    if (n_parts <= 1) return;  // finished where it lies
+    const int4 split = g.split[from];
+    const int b = split.x, h = split.y, n_parts = split.z;
+    if (n_parts <= 1 || r % a.M >= sequence(a, b).n_new) return;
+    const int rt = r / kRows;
+    // a segment's first part is the second partial of its CTA (of the segment that CTA ends in), the
+    // others are the first of theirs
     auto part = [&](int c) {
         return (2 * (static_cast<int64_t>(from + c) * g.row_tiles + rt) + (c == 0 ? 1 : 0)) * kRows + r % kRows;
     };
+    for (int c = threadIdx.x; c < n_parts; c += kJoinThreads) part_s[c] = g.stats[part(c)];
+    __syncthreads();
     const int grp = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * 4;
     Joined j;
-    for (int c = grp; c < n_parts; c += GROUPS) j.top(g.stats[part(c)].x);
-    for (int c = grp; c < n_parts; c += GROUPS) {
-        const float4 st = g.stats[part(c)];
-        j.weight(st.x, st.z);
-    }
+    for (int c = grp; c < n_parts; c += GROUPS) j.top(part_s[c].x);
+    for (int c = grp; c < n_parts; c += GROUPS) j.weight(part_s[c].x, part_s[c].z);
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
     for (int c = grp; c < n_parts; c += GROUPS) {
-        const int64_t at = part(c);
-        const float4 st = g.stats[at];
-        add_scaled(sum, *reinterpret_cast<const float4 *>(g.acc + at * D + ch), j.add(st.x, st.y, st.z));
+        const float4 st = part_s[c];
+        add_scaled(sum, *reinterpret_cast<const float4 *>(g.acc + part(c) * D + ch), j.add(st.x, st.y, st.z));
     }
     acc_s[grp][threadIdx.x % LANES] = sum;
     if (ch == 0) stat_s[grp] = make_float3(j.m, j.l, j.w);
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __gr
     const AttendLaunch &a = ct.a;
     if (blockIdx.x == 0) {
         plan_rest(ct);
-        check_attend(a);
+        check_attend<true>(a);
         return;
     }
     const int pages = static_cast<int>(ct.cap / a.pool.block);
@@ -864,7 +868,7 @@ bool attend_few_rows(int group, int M, int64_t capacity) {
     return attend_rows(group, M) <= (capacity <= kWholeTokens ? 128 : 64);
 }
 
-size_t attend_few_workspace(int B, int d, int sms) { return few_layout(B, d, few_ctas(sms)).total; }
+size_t attend_few_workspace(int d, int sms) { return few_layout(d, few_ctas(sms)).total; }
 
 template <int D, int STEP>
 static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
@@ -877,7 +881,7 @@ static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&work, attend_few_kernel<D, STEP>, g);
     if (e != cudaSuccess || g.whole) return e;
     cudaLaunchConfig_t cfg = early_launch(
-        dim3(static_cast<unsigned>(a.pool.heads * attend_rows(a.group, a.M)), static_cast<unsigned>(a.B)), kJoinThreads, 0, stream);
+        dim3(static_cast<unsigned>(attend_rows(a.group, a.M)), static_cast<unsigned>(g.ctas)), kJoinThreads, 0, stream);
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, g);
 }
 
@@ -887,13 +891,14 @@ cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream) {
     g.row_tiles = static_cast<int>(ceil_div(attend_rows(a.group, a.M), kRows));
     g.whole = static_cast<int64_t>(a.pool.max_pages) * a.pool.block <= kWholeTokens;
     const int most = few_ctas(a.sms);
-    const FewWorkspace w = few_layout(a.B, a.pool.d, most);
+    if (most > kMostCtas) return cudaErrorInvalidValue;
+    const FewWorkspace w = few_layout(a.pool.d, most);
     g.ctas = g.whole ? a.B * a.pool.heads : most / g.row_tiles;
     const int step = g.row_tiles == 1 ? kOneTileStep : kMoreTilesStep;
     g.unit = step * kWarps;
     g.log2_block = a.pool.block == 128 ? 7 : 6;
     char *ws = static_cast<char *>(a.workspace);
-    g.plan = reinterpret_cast<int32_t *>(ws + w.plan);
+    g.split = reinterpret_cast<int4 *>(ws + w.split);
     g.stats = reinterpret_cast<float4 *>(ws + w.stats);
     g.acc = reinterpret_cast<float *>(ws + w.acc);
     g.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.pool.d)));
