@@ -23,6 +23,9 @@
 //   walks the heads, the next head's rows in flight.  (With a CTA per head, each computing its
 //   angles, 4680 tokens of 40 heads, d 128, took 85 us; with as many CTAs as there are groups of
 //   5 heads, which leaves the last wave of them mostly empty, 61.)
+// Measured: those 4680 tokens 39 us, 3.7 TB/s (a head's maximum needs a barrier of the CTA before its
+// rounding, and with one CTA of 1024 threads an SM nothing else runs meanwhile: 62 % of the issue slots);
+// 333 ragged tokens of 5 sequences 5.9 us, one token 4.1 us: latency.
 // The CTA behind the last does no work of its own: it checks starts, counts and page table entries
 // and writes the status word, so that the call is one launch.
 #include <cuda_bf16.h>

@@ -51,8 +51,8 @@ struct RopeTable {
 };
 
 // Cosine and sine of pos steps.  A position is a whole number, so whole revolutions drop out of the
-// 64-bit product by themselves, and the angle is exact but for the rounding of the step (2^-65 of
-// a revolution each, 1e-9 radians at 2^31).  Of its upper 32 bits the first two, rounded, are the
+// 64-bit product by themselves, and the angle is exact but for the step's last bit (2^-64 of a
+// revolution, 1e-9 radians at 2^31).  Of its upper 32 bits the first two, rounded, are the
 // quarter turn; the rest is an angle x in [-pi/4, pi/4), good to 2^-24 of itself, whose sine
 // and cosine come from their Taylor series up to x^9 and x^8 (what is left out is below 2e-9 and
 // 3e-8).  (The same through fp64 products and sincospif took most of an append's time.)
