@@ -450,6 +450,10 @@ def test_attend_wide_batch():
     lens = [int(x) for x in rng.integers(0, 90, 70)]
     lens[3], lens[40] = 1300, 640
     attend_case(rng, 70, 1, 1, 1, 64, 64, lens, None, True)
+    # short caches, a CTA each: more of them than there are SMs
+    lens = [int(x) for x in rng.integers(0, 257, 80)]
+    attend_case(rng, 80, 2, 2, 1, 64, 64, lens, None, True)
+    attend_case(rng, 5, 2, 5, 24, 64, 64, [256, 24, 1, 130, 70], [24, 24, 1, 3, 0], True)
 
 
 def test_append_many_items():

@@ -65,8 +65,10 @@ namespace fvattn {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;  // of a CTA.  Short caches in so few CTAs that each has an SM to itself: 8, which halves
+                           // the steps one after another (64 CTAs, 500 tokens, d 128: 7.7 us, with 4 8.6; 90 tokens
+                           // 6.1 and 5.8; in a second wave, 160 CTAs, it loses: 14.2 and 10.4).
+constexpr int kMoreWarps = 8;
 constexpr int kRows = 8;                // rows of a tile
 // Tokens a warp takes at a time (inside one page: pages hold 64 or 128); a unit is what the CTA's
 // warps take.  One row tile, bound by HBM: 32, whose finer cut of the work balances better (8 x 40
@@ -166,9 +168,9 @@ __device__ __forceinline__ int units_of(const FewArgs &g, int len) {
 // The plan, in shared memory: first[b] = what comes before sequence b, for b = 0 .. B, in units
 // (stretches) or in chunks of at most first[B + 1] units; first[B + 1] = 0 says stretches.
 // Every CTA makes the same plan in its shared memory: all load the lengths, one warp adds.
-__device__ void make_plan(const FewArgs &g, int *first, int *lens) {
+__device__ __forceinline__ void make_plan(const FewArgs &g, int *first, int *lens) {
     const AttendLaunch &a = g.a;
-    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
         const Seq seq = sequence(a, b);
         lens[b] = seq.n_new > 0 ? seq.len : 0;  // (nothing to write)
     }
@@ -314,20 +316,20 @@ __device__ __forceinline__ void copies_wait() {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int D, int STEP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const __grid_constant__ FewArgs g) {
+template <int D, int STEP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == kWarps ? kCtasPerSm : 1) attend_few_kernel(const __grid_constant__ FewArgs g) {
     constexpr int KW = D / 16;      // words of a lane's part of a query or key row
     constexpr int MT = D / 16;      // m16 tiles of V^T P^T
     constexpr int VW = D / 32;      // words of a lane's V row
     constexpr int ST = STEP / 16;   // 16-token tiles of a step
-    constexpr int UNIT = STEP * kWarps;
+    constexpr int UNIT = STEP * WARPS, THREADS = WARPS * 32;
     using S_ = Step<D, STEP>;
     extern __shared__ __align__(128) unsigned char smem[];  // whole lines (16 bytes off: 142 -> 159 us)
     unsigned char *kr = smem + (threadIdx.x >> 5) * 2 * S_::BYTES, *vr = kr + S_::BYTES;  // this warp's K and V
-    float *acc_s = reinterpret_cast<float *>(smem);  // [kWarps][kRows][D], between segments
-    int *first = reinterpret_cast<int *>(smem + kWarps * 2 * S_::BYTES);
+    float *acc_s = reinterpret_cast<float *>(smem);  // [WARPS][kRows][D], between segments
+    int *first = reinterpret_cast<int *>(smem + WARPS * 2 * S_::BYTES);
     int *lens = first + g.a.B + 2;
-    __shared__ float4 stat_s[kWarps][kRows];
+    __shared__ float4 stat_s[WARPS][kRows];
     __shared__ int4 split_s;
     static_assert(kRows * D * 4 <= 2 * S_::BYTES, "the sums reuse the steps' place");
     const AttendLaunch &a = g.a;
@@ -404,9 +406,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
             const int p = checked_page(table[tok >> g.log2_block], a.pool.num_pages);
             return p < 0 ? -1 : static_cast<int64_t>(p) * H + h;
         };
-        // this warp's step at tok is on its way (copy groups K, V); the page of the next is looked up
+        // this warp's step at tok is on its way (copy groups K, V); the page of the next is looked up.  (The
+        // table is read before the length says whether its entry counts, so that the two loads overlap.)
         int tok = off * UNIT + warp * STEP;
-        int64_t ph = page_at(tok), ph_next = page_at(tok + UNIT);
+        const int entry = table[min(tok >> g.log2_block, a.pool.max_pages - 1)];
+        const int entry_next = table[min((tok + UNIT) >> g.log2_block, a.pool.max_pages - 1)];
+        const int p0 = tok < c1 ? checked_page(entry, a.pool.num_pages) : -1;
+        const int p1 = tok + UNIT < c1 ? checked_page(entry_next, a.pool.num_pages) : -1;
+        int64_t ph = p0 < 0 ? -1 : static_cast<int64_t>(p0) * H + h;
+        int64_t ph_next = p1 < 0 ? -1 : static_cast<int64_t>(p1) * H + h;
         int ek = 0, ev = 0;
         {
             const int64_t at = (ph * BS + (tok & (BS - 1))) * D + lane * 16;
@@ -682,16 +690,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_few_kernel(const 
         __syncthreads();
         const bool complete = n_units == all;
         const int slot = 2 * cta + (off == 0 ? 1 : 0);
-        for (int y = threadIdx.x; y < rows * (D / 4); y += kThreads) {
+        for (int y = threadIdx.x; y < rows * (D / 4); y += THREADS) {
             const int rr = y / (D / 4), ch = (y % (D / 4)) * 4;
             Joined j;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) j.top(stat_s[k][rr].x);
+            for (int k = 0; k < WARPS; ++k) j.top(stat_s[k][rr].x);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) j.weight(stat_s[k][rr].x, stat_s[k][rr].z);
+            for (int k = 0; k < WARPS; ++k) j.weight(stat_s[k][rr].x, stat_s[k][rr].z);
             float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
+            for (int k = 0; k < WARPS; ++k) {
                 const float4 st = stat_s[k][rr];
                 add_scaled(sum, *reinterpret_cast<const float4 *>(acc_s + (k * kRows + rr) * D + ch), j.add(st.x, st.y, st.z));
             }
@@ -875,15 +883,16 @@ bool attend_few_rows(int group, int M, int64_t capacity) {
 
 size_t attend_few_workspace(int d, int sms) { return few_layout(d, few_ctas(sms)).total; }
 
-template <int D, int STEP>
-static cudaError_t launch_few_t(const FewArgs &g, cudaStream_t stream) {
+template <int D, int STEP, int WARPS>
+static cudaError_t launch_few_t(FewArgs g, cudaStream_t stream) {
     const AttendLaunch &a = g.a;
-    constexpr size_t steps = static_cast<size_t>(kWarps) * 2 * Step<D, STEP>::BYTES;
+    g.unit = STEP * WARPS;
+    constexpr size_t steps = static_cast<size_t>(WARPS) * 2 * Step<D, STEP>::BYTES;
     const size_t smem = steps + (2 * static_cast<size_t>(a.B) + 2) * sizeof(int);
-    cudaError_t e = allow_shared_memory<attend_few_kernel<D, STEP>>(static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
+    cudaError_t e = allow_shared_memory<attend_few_kernel<D, STEP, WARPS>>(static_cast<int>(steps + (2 * kMaxHeads + 2) * sizeof(int)));
     if (e != cudaSuccess) return e;
-    const cudaLaunchConfig_t work = early_launch(dim3(static_cast<unsigned>(g.ctas * g.row_tiles) + 1), kThreads, smem, stream);
-    e = cudaLaunchKernelEx(&work, attend_few_kernel<D, STEP>, g);
+    const cudaLaunchConfig_t work = early_launch(dim3(static_cast<unsigned>(g.ctas * g.row_tiles) + 1), WARPS * 32, smem, stream);
+    e = cudaLaunchKernelEx(&work, attend_few_kernel<D, STEP, WARPS>, g);
     if (e != cudaSuccess || g.whole) return e;
     cudaLaunchConfig_t cfg = early_launch(
         dim3(static_cast<unsigned>(attend_rows(a.group, a.M)), static_cast<unsigned>(g.ctas)), kJoinThreads, 0, stream);
@@ -899,17 +908,19 @@ cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream) {
     if (most > kMostCtas) return cudaErrorInvalidValue;
     const FewWorkspace w = few_layout(a.pool.d, most);
     g.ctas = g.whole ? a.B * a.pool.heads : most / g.row_tiles;
-    const int step = g.row_tiles == 1 ? kOneTileStep : kMoreTilesStep;
-    g.unit = step * kWarps;
     g.log2_block = a.pool.block == 128 ? 7 : 6;
     char *ws = static_cast<char *>(a.workspace);
     g.split = reinterpret_cast<int4 *>(ws + w.split);
     g.stats = reinterpret_cast<float4 *>(ws + w.stats);
     g.acc = reinterpret_cast<float *>(ws + w.acc);
     g.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.pool.d)));
-    if (a.pool.d == 128)
-        return g.row_tiles == 1 ? launch_few_t<128, kOneTileStep>(g, stream) : launch_few_t<128, kMoreTilesStep>(g, stream);
-    return g.row_tiles == 1 ? launch_few_t<64, kOneTileStep>(g, stream) : launch_few_t<64, kMoreTilesStep>(g, stream);
+    const bool alone = g.whole && static_cast<int64_t>(g.ctas) * g.row_tiles < a.sms;
+#define FVATTN_FEW(D_) \
+    (alone               ? launch_few_t<D_, kOneTileStep, kMoreWarps>(g, stream) \
+     : g.row_tiles == 1 ? launch_few_t<D_, kOneTileStep, kWarps>(g, stream) \
+                         : launch_few_t<D_, kMoreTilesStep, kWarps>(g, stream))
+    return a.pool.d == 128 ? FVATTN_FEW(128) : FVATTN_FEW(64);
+#undef FVATTN_FEW
 }
 
 cudaError_t launch_cache_expand(const CacheTiles &ct, cudaStream_t stream) {
