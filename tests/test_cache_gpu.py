@@ -513,3 +513,35 @@ def test_attend_refuses_on_the_gpu():
     assert e.value.status == fv.FVATTN_ERR_CAPACITY
     with pytest.raises(ValueError):
         fv.fvattn_cache_append(Q, Q, pages, table, lens, positions=i32([[0]]))
+
+
+@pytest.mark.parametrize("M", [1, 90])
+def test_offsets_past_32_bits(M):
+    """Pages behind the pool's first 2^32 bytes, and a table so wide that the expanded pages pass 2^31 elements."""
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(71)
+    H, d, block, n_pages = 8, 128, 128, (1 << 32) // (8 * 128 * 128) + 9
+    small, _ = random_pool(rng, 4, H, block, d)
+    big = fv.KvPages(torch.empty((n_pages, H, block, d), dtype=torch.uint8, device="cuda"),
+                     torch.zeros((n_pages, H), dtype=torch.int32, device="cuda"),
+                     torch.empty((n_pages, H, block, d), dtype=torch.uint8, device="cuda"),
+                     torch.zeros((n_pages, H), dtype=torch.int32, device="cuda"))
+    wide = 16400 if M > 64 else 5     # 8 heads * 16400 pages * 128 tokens * 128 channels: past 2^31
+    table = np.full((1, wide), n_pages - 1, np.int32)
+    table[0, :4] = n_pages - 1 - np.arange(4)
+    for s, b in zip(small, big):
+        b[n_pages - 4:] = s.flip(0)
+    start = i32([300])
+    K, V = bf16(rng, 1, H, M, d), bf16(rng, 1, H, M, d)
+    for pages, t in ((small, i32([[0, 1, 2, 3]])), (big, i32(table))):
+        fv.check_status(fv.fvattn_cache_append(K, V, pages, t, start), "append")
+    for s, b in zip(small, big):
+        assert torch.equal(b[n_pages - 4:].flip(0), s)
+    Q = bf16(rng, 1, H, M, d)
+    lens = start + M
+    (kv, ke), (vv, ve) = ((ref.VALUES[c.cpu().numpy()], e.cpu().numpy()) for c, e in (small[:2], small[2:]))
+    want = ref.attend(Q.double().cpu().numpy(), kv, ke, vv, ve, np.arange(4)[None], [300 + M], [M], True)
+    for pages, t in ((small, i32([[0, 1, 2, 3]])), (big, i32(table))):
+        O, LSE, st = fv.fvattn_cache_attend(Q, pages, t, lens, causal=True)
+        fv.check_status(st, "attend")
+        check_attend(O, LSE, want, [M], 300 + M, M, d)

@@ -203,3 +203,20 @@ def test_training_step_with_positions():
     for i in range(3):
         want, got = leaf.grad[:, :, i], grad[:, :, i].double()
         assert (got - want).norm() / want.norm() < 2e-2
+
+
+def test_rope_offsets_past_32_bits():
+    """Tokens 2^22 elements apart: the last ones begin past 2^31 elements."""
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(19)
+    N, step = 600, 1 << 22
+    x = torch.empty(N * step, dtype=torch.bfloat16, device="cuda").as_strided((1, 2, N, 64), (0, 64, step, 1))
+    Q, _ = make(rng, 1, 2, N, 64, "bhnd")
+    x.copy_(Q)
+    rope = fv.rope_axes((24, 20, 20))
+    pos = fv.grid_positions(3, 10, 20)
+    want, _ = fv.fvattn_rope(Q, None, pos, rope)
+    got, _ = fv.fvattn_rope(x, None, pos, rope)
+    assert torch.equal(got, want)
+    fv.fvattn_rope(x, None, pos, rope, out_q=x)
+    assert torch.equal(x, want)
