@@ -5,7 +5,7 @@
 // Why not ctypes, as for the other calls: these run for single tokens, where the GPU is
 // done in a few microseconds.  fvattn_rope on [1, 2, 512, 64] took 29 us of host time through
 // ctypes (18 us of Python around it, 3.6 us of converting 22 arguments); from here it takes
-// 5.4, an append of one token 6.9, its attention 6.6 (two or three us of each are the launch).
+// 5.4, an append of one token 6.8, its attention 5.8 (two or three us of each are the launch).
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

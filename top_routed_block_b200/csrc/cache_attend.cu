@@ -772,11 +772,14 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
 // ---------------------------------------------------------------- pages as bf16
 
 // Every cached token of every head as bf16 (exact: a code has 4 bits, its scale is a power of
-// two), for the 128-row tiles of the tensor cores.  CTA = (page, head, sequence); CTA 0 only
+// two), for the 128-row tiles of the tensor cores.  A CTA takes pages of one (sequence, head); CTA 0 only
 // checks.  Tokens from the sequence's end to the next multiple of 128 are zeros: the tiles read
 // them.  NaN codes of V become zero in the copy and the first of each channel is kept in
 // nan_first, so that a NaN that a query does not see cannot reach it through 0 * NaN.
 constexpr int kExpandThreads = 256;
+// CTAs for each SM at most; those of a head take its pages in turn.  (A CTA a page: 8 x 8 heads with 16 of
+// 1024 pages in use 82 us, now 26; 40 heads with 256 of 256, 162 and 165.)
+constexpr int kExpandPerSm = 64;
 
 // By the checking CTA: key tiles (at least one each) before each of the rest items.
 __device__ void plan_rest(const CacheTiles &ct) {
@@ -811,24 +814,11 @@ __device__ __forceinline__ uint4 expand8(uint2 codes, int e, bool plain, float f
 }
 
 template <int D>
-__global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __grid_constant__ CacheTiles ct) {
+__device__ __forceinline__ void expand_page(const CacheTiles &ct, const Seq &seq, int b, int h, int pg) {
     constexpr int PER_ROW = D / 8, AHEAD = 64 * PER_ROW / kExpandThreads;  // a vector: 8 codes; 64 rows at a time
     const AttendLaunch &a = ct.a;
-    if (blockIdx.x == 0) {
-        plan_rest(ct);
-        check_attend<true>(a);
-        return;
-    }
-    const int pages = static_cast<int>(ct.cap / a.pool.block);
-    int64_t x = static_cast<int64_t>(blockIdx.x) - 1;
-    const int pg = static_cast<int>(x % pages);
-    x /= pages;
-    const int h = static_cast<int>(x % a.pool.heads);
-    const int b = static_cast<int>(x / a.pool.heads);
     const int BS = a.pool.block;
-    const Seq seq = sequence(a, b);
     const int tok0 = pg * BS;
-    if (seq.n_new == 0 || tok0 >= static_cast<int>(align_up(static_cast<size_t>(seq.len), 128))) return;
     const int fill = max(min(seq.len - tok0, BS), 0);  // cached slots of the page
     const int page =
         fill > 0 ? checked_page(a.pool.table[static_cast<int64_t>(b) * a.pool.max_pages + pg], a.pool.num_pages) : -1;
@@ -865,6 +855,23 @@ __global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __gr
             dst[at] = expand8(c[i], e, plain, f);
         }
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kExpandThreads) cache_expand_kernel(const __grid_constant__ CacheTiles ct, int per_head) {
+    const AttendLaunch &a = ct.a;
+    if (blockIdx.x == 0) {
+        plan_rest(ct);
+        check_attend<true>(a);
+        return;
+    }
+    const int x = static_cast<int>(blockIdx.x) - 1, bh = x / per_head;
+    const int b = bh / a.pool.heads, h = bh % a.pool.heads;
+    const Seq seq = sequence(a, b);
+    if (seq.n_new == 0) return;
+    const int pages = static_cast<int>(align_up(static_cast<size_t>(seq.len), 128)) / a.pool.block;
+#pragma unroll 1
+    for (int pg = x % per_head; pg < pages; pg += per_head) expand_page<D>(ct, seq, b, h, pg);
 }
 
 // CTAs that take work: the resident ones but for the one that checks.
@@ -925,9 +932,12 @@ cudaError_t launch_attend_few(const AttendLaunch &a, cudaStream_t stream) {
 
 cudaError_t launch_cache_expand(const CacheTiles &ct, cudaStream_t stream) {
     const AttendLaunch &a = ct.a;
-    const unsigned ctas = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.pool.heads * (ct.cap / a.pool.block) + 1);
-    if (a.pool.d == 128) cache_expand_kernel<128><<<ctas, kExpandThreads, 0, stream>>>(ct);
-    else cache_expand_kernel<64><<<ctas, kExpandThreads, 0, stream>>>(ct);
+    const int64_t heads = static_cast<int64_t>(a.B) * a.pool.heads, pages = ct.cap / a.pool.block;
+    const int64_t even = ceil_div(static_cast<int64_t>(a.sms) * kExpandPerSm, heads);
+    const int per_head = static_cast<int>(ceil_div(pages, ceil_div(pages, even)));  // equal shares
+    const unsigned ctas = static_cast<unsigned>(heads * per_head + 1);
+    if (a.pool.d == 128) cache_expand_kernel<128><<<ctas, kExpandThreads, 0, stream>>>(ct, per_head);
+    else cache_expand_kernel<64><<<ctas, kExpandThreads, 0, stream>>>(ct, per_head);
     return cudaGetLastError();
 }
 
