@@ -225,9 +225,15 @@ __device__ __forceinline__ int find_sequence(const int *first, int B, int x) {
 // ------------------------------------------------------------------ a row's sums
 
 // l = sum 2^(s - m), acc = 2^15 sum 2^(s - m + ev - w) v.  Without a token m = w = -inf, both are 0.
-__device__ __forceinline__ float out_factor(float l, float w) {
-    return l == 0.0f ? 0.0f : ex2(w - kWeightLog2) / l;
-}
+// acc 2^(w - 15) / l, the power of two in two factors: w goes with V's exponents, and 2^(w - 15) alone may
+// lie outside fp32 where the result does not (a page of values near 2^-120, or a channel of zeros in a
+// page of exponent 200).
+struct OutFactor {
+    float inv_l, half;
+    __device__ __forceinline__ OutFactor(float l, float w)
+        : inv_l(l == 0.0f ? 0.0f : 1.0f / l), half(l == 0.0f ? 0.0f : ex2((w - kWeightLog2) * 0.5f)) {}
+    __device__ __forceinline__ float operator()(float acc) const { return acc * inv_l * half * half; }
+};
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
@@ -255,10 +261,10 @@ __device__ __forceinline__ void add_scaled(float4 &sum, const float4 &v, float f
 __device__ __forceinline__ void write_row(const AttendLaunch &a, int b, int h, int r, int ch, const float4 &sum,
                                           const Joined &j) {
     const int64_t hq = h * a.group + r / a.M, tok = r % a.M;
-    const float f = out_factor(j.l, j.w);
+    const OutFactor f(j.l, j.w);
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.O) + b * a.o_b + hq * a.o_h + tok * a.o_n + ch;
-    const __nv_bfloat162 p0 = __floats2bfloat162_rn(sum.x * f, sum.y * f);
-    const __nv_bfloat162 p1 = __floats2bfloat162_rn(sum.z * f, sum.w * f);
+    const __nv_bfloat162 p0 = __floats2bfloat162_rn(f(sum.x), f(sum.y));
+    const __nv_bfloat162 p1 = __floats2bfloat162_rn(f(sum.z), f(sum.w));
     *reinterpret_cast<uint2 *>(out) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&p0), *reinterpret_cast<const uint32_t *>(&p1));
     if (ch == 0) a.LSE[(static_cast<int64_t>(b) * a.pool.heads * a.group + hq) * a.M + tok] = lse_of(j.m, j.l);
