@@ -93,3 +93,21 @@ def test_channels_of_zeros_beside_values_past_fp32(M, ev):
         far = np.abs(o) > 2.0 ** 128
         got = O.double().cpu().numpy()
         assert far.sum() > M * 64 and np.array_equal(got[far], np.copysign(np.inf, o[far]))
+
+
+@pytest.mark.parametrize("M", FEW + MANY)
+def test_large_queries_and_keys_in_different_channels(M):
+    """Products that are zero, whose scales multiply to more than fp32 holds."""
+    rng = np.random.default_rng(M)
+    pages, table = pool(rng, 64, ek=110)
+    pages.k_codes[..., :32] = 0
+    Q = bf16(rng, 1, 2, M, 64) * 2.0 ** 110
+    Q[..., 32:] = 0
+    check(Q, run(Q, pages, table, [570]), plain_of(pages), table, [570], few=M in FEW)
+    # one channel in common, with small keys: scores of ordinary size
+    pages, table = pool(rng, 64, ek=-113)
+    pages.k_codes[..., :31] = 0
+    Q = bf16(rng, 1, 2, M, 64) * 2.0 ** 110
+    Q[..., 32:] = 0
+    pages.k_codes[..., 32:] = 0
+    check(Q, run(Q, pages, table, [570]), plain_of(pages), table, [570], few=M in FEW)

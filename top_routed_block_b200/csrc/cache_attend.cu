@@ -81,6 +81,7 @@ constexpr int kChunkShare = 8;          // units per CTA below which segments ar
 constexpr int kChunkSequences = 64;     // more sequences are not worth the search for the chunk
 constexpr int kMostCtas = 512;          // stretches (444 CTAs are resident on 148 SMs)
 constexpr int kJoinThreads = 128;
+constexpr int kMostScale = 125;         // largest power of two in the scores' factor
 constexpr float kWeightLog2 = 15.0f;    // weights are scaled by 2^15 before fp16
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -560,7 +561,13 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kWarps ? kCtasPerSm : 1) 
             bool moved = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float f = scale_pow2(g.scale_log2, clamp_exp(sqr[e] + ek_here));
+                const int fe = clamp_exp(sqr[e] + ek_here);
+                const float f = scale_pow2(g.scale_log2, min(fe, kMostScale));
+                if (fe > kMostScale) {  // what is above that on its own, so that a product of zero stays zero
+                    const float above = __int_as_float((fe - kMostScale + 127) << 23);
+#pragma unroll
+                    for (int mt = 0; mt < ST; ++mt) s[mt][e] *= above, s[mt][2 + e] *= above;
+                }
                 float mx = kNegInf;
 #pragma unroll
                 for (int mt = 0; mt < ST; ++mt)
