@@ -542,9 +542,13 @@ FVATTN_API size_t fvattn_cache_attend_workspace_bytes(int B, int heads, int grou
  * A query that sees no token (an empty sequence) gets O = 0 and LSE = -inf.  What a query does
  * not see, NaN codes and places behind the sequence's end among it, does not reach its row.
  * Few rows (as above): the weights are rounded to fp16 before P V and the cached tokens are
- * split over the SMs and joined in a fixed order.  More: the pages are expanded to bf16 (exact) in
- * the workspace and the tensor cores' 128-row tiles run over them, with P rounded to bf16 as in
- * fvattn_sparse_fwd.  Both sum in fp32.  The result does not depend on what else runs; no atomics
+ * split over the SMs and joined in a fixed order; a token counts down to 2^-40 of the row's largest
+ * P 2^exponent.  More: the pages are expanded to bf16 in the workspace and the tensor cores' 128-row
+ * tiles run over them, with P rounded to bf16 as in fvattn_sparse_fwd.  That is exact for keys and
+ * values that are multiples of 2^-133 (exponents of -124 and more); smaller ones are rounded to it, and what is
+ * above bf16's largest number, 255 * 2^120, counts as that (append writes one such value, 256 * 2^120).
+ * Both sum in fp32 (the tiles' sums of P V overflow where |V| times the tokens passes 2^128, as in
+ * fvattn_sparse_fwd).  The result does not depend on what else runs; no atomics
  * on floating values.  Exponents outside [-250, 250] are taken as the nearer end.
  * *dev_status (written by the call): FVATTN_ERR_BAD_PAGE where lens is outside [0, max_pages *
  * block], new_lens outside [0, M] (both are clamped), or a page table entry of a sequence's cached

@@ -70,7 +70,7 @@ def test_small_and_large_values_few_rows(d, M, n, ev):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("M", MANY)
-@pytest.mark.parametrize("ev", [-110, 100, 110])   # (sums of values near 2^128 overflow, as the forward's do)
+@pytest.mark.parametrize("ev", [-124, -119, -110, 100, 110])   # (sums of values near 2^128 overflow, as the forward's do)
 def test_small_and_large_values_many_rows(d, M, ev):
     rng = np.random.default_rng(M)
     pages, table = pool(rng, d, ev=ev)
@@ -93,6 +93,54 @@ def test_channels_of_zeros_beside_values_past_fp32(M, ev):
         far = np.abs(o) > 2.0 ** 128
         got = O.double().cpu().numpy()
         assert far.sum() > M * 64 and np.array_equal(got[far], np.copysign(np.inf, o[far]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("M", FEW + MANY)
+def test_large_appended_value_that_a_row_does_not_see(d, M):
+    """A finite bf16 value appended as 256 * 2^120 = 2^128: rows before it are as if it were zero, rows that see
+    it have a finite result."""
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(d + M)
+    L, block = 512 + M, 64
+    pages, _ = random_pool(rng, 12, 2, block, d)
+    table = [list(range(12))]
+    u = L - M + M // 2   # seen by query tokens M // 2 and later
+    pages.v_exp[u // block] = 120
+    pages.v_codes[u // block] = 0
+    Q = bf16(rng, 1, 2, M, d)
+    clean = run(Q, pages, table, [L])
+    if u % block == 0:   # (append finds the page empty)
+        pages.v_exp[u // block] = -160
+    V = torch.zeros(1, 2, 1, d, dtype=torch.bfloat16, device="cuda")
+    V[..., 3], V[..., 40] = 3.3e38, -3.35e38
+    K = bf16(rng, 1, 2, 1, d)
+    keep = [t.clone() for t in pages[:2]]
+    fv.check_status(fv.fvattn_cache_append(K, V, pages, i32(table), i32([u])), "append")
+    for a, b in zip(pages[:2], keep):
+        a.copy_(b)
+    assert (pages.v_exp[u // block] == 120).all() and (pages.v_codes[u // block, :, u % block, 3] == CODE_256).all()
+    got = run(Q, pages, table, [L])
+    assert torch.equal(got[0][:, :, : M // 2], clean[0][:, :, : M // 2]) and torch.equal(got[1], clean[1])
+    plain = plain_of(pages)
+    if M in MANY:
+        plain[1][0][np.abs(plain[1][0]) * 2.0 ** plain[1][1][..., None, None].astype(float) >= 2.0 ** 128] *= 255 / 256
+    check(Q, got, plain, table, [L], few=M in FEW)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("M", FEW + MANY)
+def test_keys_of_2_128_and_small_queries(d, M):
+    """Keys at the upper end, queries so small that the scores are ordinary numbers."""
+    rng = np.random.default_rng(d + M)
+    pages, table = pool(rng, d, ek=120)
+    pages.k_codes.bitwise_and_(0x87)            # up to 2^-6 of the scale, but for
+    pages.k_codes[:, :, ::7, 5] = CODE_256      # these
+    Q = bf16(rng, 1, 2, M, d) * 2.0 ** -118
+    plain = plain_of(pages)
+    if M in MANY:
+        plain[0][0][plain[0][0] == 256] = 255
+    check(Q, run(Q, pages, table, [570]), plain, table, [570], few=M in FEW)
 
 
 @pytest.mark.parametrize("M", FEW + MANY)

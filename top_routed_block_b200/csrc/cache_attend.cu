@@ -784,11 +784,13 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
 
 // ---------------------------------------------------------------- pages as bf16
 
-// Every cached token of every head as bf16 (exact: a code has 4 bits, its scale is a power of
-// two), for the 128-row tiles of the tensor cores.  A CTA takes pages of one (sequence, head); CTA 0 only
-// checks.  Tokens from the sequence's end to the next multiple of 128 are zeros: the tiles read
-// them.  NaN codes of V become zero in the copy and the first of each channel is kept in
-// nan_first, so that a NaN that a query does not see cannot reach it through 0 * NaN.
+// Every cached token of every head as bf16, for the 128-row tiles of the tensor cores.  Exact (a code
+// has 4 bits and its scale is a power of two) from 2^-133, bf16's smallest step, up to its largest
+// number, which stands for all above it: an infinity would reach the rows that do not see it, as
+// 0 * inf.  A CTA takes pages of one (sequence, head); CTA 0 only checks.  Tokens from the
+// sequence's end to the next multiple of 128 are zeros: the tiles read them.  NaN codes of V become
+// zero in the copy and the first of each channel is kept in nan_first, so that a NaN that a query
+// does not see cannot reach it through 0 * NaN.
 constexpr int kExpandThreads = 256;
 // CTAs for each SM at most; those of a head take its pages in turn.  (A CTA a page: 8 x 8 heads with 16 of
 // 1024 pages in use 82 us, now 26; 40 heads with 256 of 256, 162 and 165.)
@@ -811,7 +813,13 @@ __device__ void plan_rest(const CacheTiles &ct) {
     if (i == 0) ct.rest[ct.n_rest] = sums[kExpandThreads - 1];
 }
 
-// Eight codes times 2^e (f, where that is a normal number).
+constexpr float kMostBf16 = 3.38953139e38f;  // 255 2^120
+constexpr int kMostPlainExp = 119;           // 448 2^119 is below it
+
+// Inside bf16's range; a NaN stays.
+__device__ __forceinline__ float held(float x) { return x > kMostBf16 ? kMostBf16 : x < -kMostBf16 ? -kMostBf16 : x; }
+
+// Eight codes times 2^e (f, where that is a normal number and no product passes bf16's range).
 __device__ __forceinline__ uint4 expand8(uint2 codes, int e, bool plain, float f) {
     uint32_t out[4];
     const uint32_t c[4] = {codes.x & 0xffffu, codes.x >> 16, codes.y & 0xffffu, codes.y >> 16};
@@ -819,7 +827,8 @@ __device__ __forceinline__ uint4 expand8(uint2 codes, int e, bool plain, float f
     for (int i = 0; i < 4; ++i) {
         const uint32_t h = f16x2_of_codes(c[i]);
         float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v = plain ? make_float2(v.x * f, v.y * f) : make_float2(scale_pow2(v.x, e), scale_pow2(v.y, e));
+        if (plain) v = make_float2(v.x * f, v.y * f);
+        else v = make_float2(held(scale_pow2(v.x, e)), held(scale_pow2(v.y, e)));
         const __nv_bfloat162 y = __floats2bfloat162_rn(v.x, v.y);
         out[i] = *reinterpret_cast<const uint32_t *>(&y);
     }
@@ -843,7 +852,7 @@ __device__ __forceinline__ void expand_page(const CacheTiles &ct, const Seq &seq
         const bool is_v = part >= BS / 64;
         const int row0 = (is_v ? part - BS / 64 : part) * 64;
         const int e = page < 0 ? 0 : clamp_exp((is_v ? a.pool.ve : a.pool.ke)[ph]);
-        const bool plain = e >= -126 && e <= 127;
+        const bool plain = e >= -126 && e <= kMostPlainExp;
         const float f = plain ? __int_as_float((e + 127) << 23) : 0.0f;
         const uint2 *src = reinterpret_cast<const uint2 *>((is_v ? a.pool.v : a.pool.k) + (ph * BS + row0) * D);
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(is_v ? ct.V : ct.K) + (bh * ct.cap + tok0 + row0) * D);
