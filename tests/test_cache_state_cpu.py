@@ -1,0 +1,49 @@
+"""What FvattnCache and FvattnPlan keep between calls, with the device calls replaced by fakes: lengths,
+first errors, buffers."""
+import pytest
+import torch
+
+import top_routed_block_b200 as fv
+
+
+class Calls:
+    """Stands in for the device calls: writes the next of the given status words, as they do."""
+
+    def __init__(self, monkeypatch):
+        self.append, self.attend = [], []
+        monkeypatch.setattr(fv, "fvattn_cache_append", self._append)
+        monkeypatch.setattr(fv, "fvattn_cache_attend", self._attend)
+        monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
+
+    def _append(self, K, V, pages, table, start, *, dev_status, **kw):
+        dev_status[0] = self.append.pop(0) if self.append else 0
+        return dev_status
+
+    def _attend(self, Q, pages, table, lens, *, dev_status, **kw):
+        dev_status[0] = self.attend.pop(0) if self.attend else 0
+        return Q, None, dev_status
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    return Calls(monkeypatch)
+
+
+def cache(B=3):
+    return fv.FvattnCache(B, 2, 64, 64, 256, device="cpu")
+
+
+def rows(B, T):
+    return torch.zeros(B, 2, T, 64, dtype=torch.bfloat16)
+
+
+def test_lengths_are_what_was_appended(calls):
+    """The kernel holds a count inside [0, T]; the lengths follow it."""
+    c = cache()
+    c.append(rows(3, 10), rows(3, 10))
+    assert c.lens.tolist() == [10, 10, 10]
+    given = torch.tensor([11, -4, 3], dtype=torch.int32)
+    c.append(rows(3, 10), rows(3, 10), new_lens=given)
+    assert c.lens.tolist() == [20, 10, 13] and given.tolist() == [11, -4, 3]
+    c.append(rows(3, 1), rows(3, 1), new_lens=torch.tensor([-(2 ** 31), 2 ** 31 - 1, 0], dtype=torch.int32))
+    assert c.lens.tolist() == [20, 11, 13]

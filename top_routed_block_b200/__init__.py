@@ -631,10 +631,11 @@ class FvattnCache:
         self.status = torch.zeros(2, dtype=torch.int32, device=dev)   # append, attention
 
     def append(self, K, V, *, new_lens=None, positions=None, rope=None):
-        """Appends K and V (bf16 [B, heads, T, d]) and moves the lengths on (current stream)."""
+        """Appends K and V (bf16 [B, heads, T, d]) and moves the lengths on (current stream), by counts held
+        inside [0, T] as the call holds them."""
         fvattn_cache_append(K, V, self.pages, self.page_table, self.lens, new_lens=new_lens, positions=positions,
                             rope=rope, dev_status=self.status)
-        self.lens.add_(K.shape[2] if new_lens is None else new_lens)
+        self.lens.add_(K.shape[2] if new_lens is None else new_lens.clamp(0, K.shape[2]))
 
     def attend(self, Q, *, new_lens=None, causal=True, O=None, LSE=None):
         """Attention of the tokens appended last over all cached ones; returns (O, LSE)."""
