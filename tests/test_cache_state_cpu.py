@@ -47,3 +47,19 @@ def test_lengths_are_what_was_appended(calls):
     assert c.lens.tolist() == [20, 10, 13] and given.tolist() == [11, -4, 3]
     c.append(rows(3, 1), rows(3, 1), new_lens=torch.tensor([-(2 ** 31), 2 ** 31 - 1, 0], dtype=torch.int32))
     assert c.lens.tolist() == [20, 11, 13]
+
+
+@pytest.mark.parametrize("call,codes", [("append", [0, -8, 0, 0]), ("attend", [-7, 0]), ("attend", [0, -8, 0]), ("append", [-8])])
+def test_errors_stay_until_they_are_reported(calls, call, codes):
+    c = cache()
+    c.check()
+    getattr(calls, call).extend(codes)
+    for _ in codes:
+        c.append(rows(3, 1), rows(3, 1))
+        c.attend(rows(3, 1))
+    with pytest.raises(fv.FvattnError) as e:
+        c.check()
+    assert e.value.status == min(codes)
+    c.append(rows(3, 1), rows(3, 1))
+    c.attend(rows(3, 1))
+    c.check()

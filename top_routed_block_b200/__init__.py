@@ -628,23 +628,33 @@ class FvattnCache:
                              torch.zeros(shape[:2], dtype=torch.int32, device=dev))
         self.page_table = torch.arange(B * per_seq, dtype=torch.int32, device=dev).view(B, per_seq)
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
-        self.status = torch.zeros(2, dtype=torch.int32, device=dev)   # append, attention
+        self.status = torch.zeros(2, dtype=torch.int32, device=dev)   # append, attention: of the last call each
+        self.errors = torch.zeros(2, dtype=torch.int32, device=dev)   # the same, of all calls since check()
+
+    def _keep_errors(self):
+        torch.minimum(self.errors, self.status, out=self.errors)   # (errors are negative; one launch, also in a graph)
 
     def append(self, K, V, *, new_lens=None, positions=None, rope=None):
         """Appends K and V (bf16 [B, heads, T, d]) and moves the lengths on (current stream), by counts held
         inside [0, T] as the call holds them."""
         fvattn_cache_append(K, V, self.pages, self.page_table, self.lens, new_lens=new_lens, positions=positions,
                             rope=rope, dev_status=self.status)
+        self._keep_errors()
         self.lens.add_(K.shape[2] if new_lens is None else new_lens.clamp(0, K.shape[2]))
 
     def attend(self, Q, *, new_lens=None, causal=True, O=None, LSE=None):
         """Attention of the tokens appended last over all cached ones; returns (O, LSE)."""
         O, LSE, _ = fvattn_cache_attend(Q, self.pages, self.page_table, self.lens, new_lens=new_lens, causal=causal,
                                         O=O, LSE=LSE, dev_status=self.status[1:])
+        self._keep_errors()
         return O, LSE
 
     def check(self):
-        check_status(self.status, "fvattn cache")
+        """Synchronise and raise if any call since the last check() recorded an error."""
+        try:
+            check_status(self.errors, "fvattn cache")
+        finally:
+            self.errors.zero_()
 
 
 def fvattn_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Tensor, p: float, block: int,
