@@ -63,3 +63,23 @@ def test_errors_stay_until_they_are_reported(calls, call, codes):
     c.append(rows(3, 1), rows(3, 1))
     c.attend(rows(3, 1))
     c.check()
+
+
+def test_a_plan_allocates_the_turned_tensors_once(monkeypatch):
+    given = []
+
+    def rope(Q, K, positions, axes, *, out_q=None, out_k=None, stream=None):
+        given.append((out_q, out_k))
+        return (torch.empty_like(Q) if out_q is None else out_q, torch.empty_like(K) if out_k is None else out_k)
+
+    monkeypatch.setattr(fv, "fvattn_rope", rope)
+    monkeypatch.setattr(fv, "fvattn_route", lambda Q, K, *a, **kw: None)
+    monkeypatch.setattr(fv, "fvattn_sparse_fwd", lambda Q, K, *a, **kw: (Q, K))
+    plan = fv.FvattnPlan(1, 2, 100, 64, 64, device="cpu")
+    x = torch.zeros(1, 2, 100, 64, dtype=torch.bfloat16)
+    first = plan(x, x, x, 0.9, positions=x, rope=x)
+    assert plan.turned == first and given == [(None, None)]
+    plan(x, x, x, 0.9)
+    assert plan.turned is None
+    again = plan(x, x, x, 0.9, positions=x, rope=x)
+    assert given[1][0] is first[0] and given[1][1] is first[1] and again[0] is first[0] and plan.turned[1] is first[1]

@@ -53,3 +53,28 @@ def test_errors_and_lengths_of_a_cache():
         with pytest.raises(fv.FvattnError):
             c.check()
         c.check()
+
+
+def test_a_plan_with_positions_allocates_nothing_more():
+    import numpy as np
+    import top_routed_block_b200 as fv
+    rng = np.random.default_rng(5)
+    pos, axes = fv.grid_positions(4, 8, 8), fv.rope_axes((24, 20, 20))
+    Q, K, V = (bf16(rng, 1, 2, 256, 64, layout=x) for x in ("bnhd", "bnhd", "bhnd"))
+    plan = fv.FvattnPlan(1, 2, 256, 64, 64)
+    O = plan(Q, K, V, 0.9, positions=pos, rope=axes)[0].clone()
+    turned = [t.clone() for t in plan.turned]
+    plan(K, Q, V, 0.9, positions=pos, rope=axes)
+    torch.cuda.synchronize()
+    before, at = torch.cuda.memory_allocated(), [t.data_ptr() for t in plan.turned]
+    torch.cuda.reset_peak_memory_stats()
+    again = plan(Q, K, V, 0.9, positions=pos, rope=axes)[0]
+    plan.check()
+    assert torch.cuda.max_memory_allocated() == before and [t.data_ptr() for t in plan.turned] == at
+    assert torch.equal(again, O) and all(torch.equal(a, b) for a, b in zip(plan.turned, turned))
+    s = torch.cuda.Stream()
+    plan.O.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    plan(Q, K, V, 0.9, positions=pos, rope=axes, stream=s)
+    s.synchronize()
+    assert torch.equal(plan.O, O)

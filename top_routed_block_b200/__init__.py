@@ -585,6 +585,7 @@ class FvattnPlan:
         self.LSE = torch.empty((B, H, N), dtype=torch.float32, device=dev)
         self.status = torch.zeros(3, dtype=torch.int32, device=dev)   # route, attention, first error (host path)
         self.turned = None   # (Q, K) as attended, after a call with rotary positions
+        self._turned = (None, None)   # their buffers, from the first such call on
 
     def run_route(self, Q, K, p, stream=None) -> RouteResult:
         return fvattn_route(Q, K, p, self.block, stream=stream, out=self.route, workspace=self.route_ws)
@@ -597,12 +598,14 @@ class FvattnPlan:
 
     def __call__(self, Q, K, V, p, causal=False, stream=None, positions=None, rope=None):
         """Routing and attention; with ``positions`` and ``rope`` Q and K (any strides) are turned
-        first and stay in ``turned``, which is what fvattn_sparse_bwd takes."""
+        first and stay in ``turned``, which is what fvattn_sparse_bwd takes, until the next such call (as O
+        and LSE do)."""
         if (positions is None) != (rope is None):
             raise ValueError("positions and rope belong together")
         self.turned = None
         if rope is not None:
-            self.turned = Q, K = fvattn_rope(Q, K, positions, rope, stream=stream)
+            out_q, out_k = self._turned
+            self.turned = self._turned = Q, K = fvattn_rope(Q, K, positions, rope, out_q=out_q, out_k=out_k, stream=stream)
         self.run_route(Q, K, p, stream=stream)
         return self.run_fwd(Q, K, V, causal, stream=stream)
 
