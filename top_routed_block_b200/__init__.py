@@ -475,6 +475,10 @@ def _native_calls():
         except ImportError as e:
             raise FvattnError(FVATTN_ERR_UNSUPPORTED, f"_binding.so not built ({e}); "
                               "run python -m top_routed_block_b200._build") from e
+        from ._build import binding_target
+        if m.built_for != binding_target():
+            raise FvattnError(FVATTN_ERR_UNSUPPORTED, f"_binding.so was built for {m.built_for}, this is {binding_target()}; "
+                              "run python -m top_routed_block_b200._build")
         _native = m
     return _native
 

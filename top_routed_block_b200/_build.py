@@ -15,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfvattn.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(PKG, "_build", "binding.txt")   # the Python and torch that BINDING was compiled against
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -37,9 +38,24 @@ def _newer(paths, than: str) -> bool:
     return not os.path.exists(than) or any(os.path.getmtime(p) > os.path.getmtime(than) for p in paths)
 
 
+def binding_target() -> str:
+    """What the binding is compiled against: torch's C++ interface is another one in each release."""
+    import torch
+    return f"python {sys.version_info[0]}.{sys.version_info[1]}, torch {torch.__version__}"
+
+
+def _binding_stale() -> bool:
+    if _newer([os.path.join(PKG, "csrc", "binding.cpp"), os.path.join(ROOT, "include", "fvattn.h")], BINDING):
+        return True
+    if not os.path.exists(BUILT_FOR):
+        return True
+    with open(BUILT_FOR) as f:
+        return f.read() != binding_target()
+
+
 def _build_binding(force: bool) -> None:
     src = os.path.join(PKG, "csrc", "binding.cpp")
-    if not force and not _newer([src, os.path.join(ROOT, "include", "fvattn.h")], BINDING):
+    if not force and not _binding_stale():
         return
     import torch
     root = os.path.dirname(torch.__file__)
@@ -48,11 +64,15 @@ def _build_binding(force: bool) -> None:
     tmp = BINDING + ".tmp"
     subprocess.check_call([
         "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        f'-DFVATTN_BUILT_FOR="{binding_target()}"',
         "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
         "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
         "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", PKG, "-lfvattn", "-Wl,-rpath,$ORIGIN",
         "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BUILT_FOR), exist_ok=True)
+    with open(BUILT_FOR, "w") as f:
+        f.write(binding_target())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

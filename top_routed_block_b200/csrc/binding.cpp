@@ -343,4 +343,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Calls of libfvattn.so 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", FVATTN_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}
