@@ -466,7 +466,7 @@ FVATTN_API int fvattn_attn_work_order(const int32_t *row_ptr, const int32_t *col
  *   pos           device int32 [N, n_axes], or [B, N, n_axes] with pos_batch_stride =
  *                 N * n_axes (0: one for all sequences).  Any int32 value: angles are reduced in
  *                 64-bit fixed point.
- *   inv_freq      host double[n_pairs], finite.   pair_axis  host int32[n_pairs] in [0, n_axes).
+ *   inv_freq      host double[n_pairs], of magnitude below 2^64.   pair_axis  host int32[n_pairs] in [0, n_axes).
  *                 Both are read during the call only.
  * 1 <= n_axes <= 4; 1 <= n_pairs <= d/2, a multiple of 8 for pairing 1; d in {64, 128}; N >= 1;
  * B <= 65535.  Products in fp32, one rounding to bf16.  Asynchronous on `stream`; no workspace

@@ -18,6 +18,7 @@
 #include "lpt.cuh"
 #include "quant.cuh"
 #include "rope.cuh"
+#include "rope_step.h"
 #include "route.cuh"
 #include "sasa.cuh"
 
@@ -226,10 +227,8 @@ int make_rope(RopeParams *p, const double *inv_freq, const int32_t *pair_axis, i
     if (pairing == 1 && n_pairs % 8) return FVATTN_ERR_UNSUPPORTED;
     for (int j = 0; j < n_pairs; ++j) {
         if (!std::isfinite(inv_freq[j]) || pair_axis[j] < 0 || pair_axis[j] >= n_axes) return FVATTN_ERR_INVALID_ARG;
-        // modulo one revolution, in 2^-64 of it (long double: 64 bits)
-        const long double turns = inv_freq[j] / 6.283185307179586476925286766559L;
-        const long double part = turns - std::floor(turns);  // (1 where turns is just below 0)
-        p->step[j] = part < 1.0L ? static_cast<uint64_t>(part * 18446744073709551616.0L) : 0;
+        if (std::fabs(inv_freq[j]) >= kMostRopeFreq) return FVATTN_ERR_UNSUPPORTED;
+        p->step[j] = rope_step(inv_freq[j]);
         p->axis[j] = static_cast<uint8_t>(pair_axis[j]);
     }
     p->n_pairs = n_pairs;

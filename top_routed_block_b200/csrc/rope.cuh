@@ -13,7 +13,7 @@ constexpr int kMaxRopeAxes = 4;
 
 // By value in the kernels' parameters: what one channel pair is turned by.
 struct RopeParams {
-    uint64_t step[kMaxRopePairs];  // revolutions per unit of position, inv_freq / (2 pi), modulo 1 in 2^-64
+    uint64_t step[kMaxRopePairs];  // revolutions per unit of position, modulo 1 in 2^-64 (rope_step.h)
     uint8_t axis[kMaxRopePairs];   // which coordinate of the position turns the pair
     int n_pairs;                   // pairs that turn; 2 n_pairs <= d, the other channels pass through
     int n_axes;
