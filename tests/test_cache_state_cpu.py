@@ -13,7 +13,9 @@ class Calls:
         self.append, self.attend = [], []
         monkeypatch.setattr(fv, "fvattn_cache_append", self._append)
         monkeypatch.setattr(fv, "fvattn_cache_attend", self._attend)
+        self.captured = False
         monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.captured)
 
     def _append(self, K, V, pages, table, start, *, dev_status, **kw):
         dev_status[0] = self.append.pop(0) if self.append else 0
@@ -49,7 +51,10 @@ def test_lengths_are_what_was_appended(calls):
     assert c.lens.tolist() == [20, 11, 13]
 
 
-@pytest.mark.parametrize("call,codes", [("append", [0, -8, 0, 0]), ("attend", [-7, 0]), ("attend", [0, -8, 0]), ("append", [-8])])
+@pytest.mark.parametrize("call,codes", [
+    ("append", [0, -8, 0, 0]), ("attend", [-7, 0]), ("attend", [0, -8, 0]), ("append", [-8]),
+    ("append", [0, -8] + [0] * 700), ("attend", [0] * 127 + [-8]), ("append", [0] * 128 + [-8, 0, -7]), ("attend", [0] * 300 + [-8] + [0] * 126),
+])
 def test_errors_stay_until_they_are_reported(calls, call, codes):
     c = cache()
     c.check()
@@ -57,11 +62,36 @@ def test_errors_stay_until_they_are_reported(calls, call, codes):
     for _ in codes:
         c.append(rows(3, 1), rows(3, 1))
         c.attend(rows(3, 1))
+    assert c.status.tolist() == ([codes[-1], 0] if call == "append" else [0, codes[-1]])
     with pytest.raises(fv.FvattnError) as e:
         c.check()
     assert e.value.status == min(codes)
     c.append(rows(3, 1), rows(3, 1))
     c.attend(rows(3, 1))
+    c.check()
+
+
+def test_errors_of_captured_calls_stay(calls):
+    """A captured call writes the same word at every replay and keeps its errors itself; calls outside the graph, also
+    many of them, have other words."""
+    c = cache()
+    c.append(rows(3, 1), rows(3, 1))
+    c.check()
+    calls.captured = True
+    calls.append, calls.attend = [0, -8, 0, 0], [0, -7, 0, 0]
+    words = set()
+    for _ in range(4):
+        c.append(rows(3, 1), rows(3, 1))
+        c.attend(rows(3, 1))
+        words.add((c._last[0].data_ptr(), c._last[1].data_ptr()))
+    assert len(words) == 1
+    calls.captured = False
+    for _ in range(300):
+        c.attend(rows(3, 1))
+        assert all(c._last[1].data_ptr() not in w for w in words)
+    with pytest.raises(fv.FvattnError) as e:
+        c.check()
+    assert e.value.status == -8
     c.check()
 
 

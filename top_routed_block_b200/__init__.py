@@ -635,33 +635,64 @@ class FvattnCache:
                              torch.zeros(shape[:2], dtype=torch.int32, device=dev))
         self.page_table = torch.arange(B * per_seq, dtype=torch.int32, device=dev).view(B, per_seq)
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
-        self.status = torch.zeros(2, dtype=torch.int32, device=dev)   # append, attention: of the last call each
-        self.errors = torch.zeros(2, dtype=torch.int32, device=dev)   # the same, of all calls since check()
+        # Status words: one for each call, so that no call overwrites an error of another (one word and a launch that
+        # keeps its errors took 28 us a step of append and attend, host time; this takes 21).  The first two are of captured
+        # calls, which write the same word at each replay and bring the launch with them.
+        self._words = torch.zeros(self.STATUS_WORDS, dtype=torch.int32, device=dev)
+        self._each = list(self._words.split(1))
+        self._next = 2
+        self._last = [self._each[0], self._each[1]]
+        self._errors = torch.zeros(1, dtype=torch.int32, device=dev)   # of all calls since check() whose words are reused
 
-    def _keep_errors(self):
-        torch.minimum(self.errors, self.status, out=self.errors)   # (errors are negative; one launch, also in a graph)
+    STATUS_WORDS = 258
+
+    @property
+    def status(self) -> torch.Tensor:
+        """Status of the last append and of the last attention (int32 [2])."""
+        return torch.cat(self._last)
+
+    def _call(self, which: int, f, *args, **kw):
+        """f with the status word of its own, which: 0 append, 1 attention."""
+        captured = torch.cuda.is_current_stream_capturing()
+        if captured:
+            word = self._each[which]
+        else:
+            if self._next == self.STATUS_WORDS:
+                self._collect()
+            word = self._each[self._next]
+        r = f(*args, dev_status=word, **kw)
+        self._last[which] = word
+        if captured:
+            torch.minimum(self._errors, word, out=self._errors)   # (errors are negative)
+        else:
+            self._next += 1
+        return r
+
+    def _collect(self):
+        torch.minimum(self._errors, self._words.amin(), out=self._errors)
+        self._words.zero_()
+        self._next = 2
 
     def append(self, K, V, *, new_lens=None, positions=None, rope=None):
         """Appends K and V (bf16 [B, heads, T, d]) and moves the lengths on (current stream), by counts held
         inside [0, T] as the call holds them."""
-        fvattn_cache_append(K, V, self.pages, self.page_table, self.lens, new_lens=new_lens, positions=positions,
-                            rope=rope, dev_status=self.status)
-        self._keep_errors()
+        self._call(0, fvattn_cache_append, K, V, self.pages, self.page_table, self.lens, new_lens=new_lens,
+                   positions=positions, rope=rope)
         self.lens.add_(K.shape[2] if new_lens is None else new_lens.clamp(0, K.shape[2]))
 
     def attend(self, Q, *, new_lens=None, causal=True, O=None, LSE=None):
         """Attention of the tokens appended last over all cached ones; returns (O, LSE)."""
-        O, LSE, _ = fvattn_cache_attend(Q, self.pages, self.page_table, self.lens, new_lens=new_lens, causal=causal,
-                                        O=O, LSE=LSE, dev_status=self.status[1:])
-        self._keep_errors()
+        O, LSE, _ = self._call(1, fvattn_cache_attend, Q, self.pages, self.page_table, self.lens, new_lens=new_lens,
+                               causal=causal, O=O, LSE=LSE)
         return O, LSE
 
     def check(self):
         """Synchronise and raise if any call since the last check() recorded an error."""
+        self._collect()
         try:
-            check_status(self.errors, "fvattn cache")
+            check_status(self._errors, "fvattn cache")
         finally:
-            self.errors.zero_()
+            self._errors.zero_()
 
 
 def fvattn_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Tensor, p: float, block: int,
