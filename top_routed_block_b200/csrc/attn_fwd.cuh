@@ -47,7 +47,8 @@ cudaError_t launch_item_order(const int32_t *row_ptr, int64_t BH, int nb, int32_
 cudaError_t launch_natural_order(int64_t n, int32_t *order, cudaStream_t stream);
 int attn_ctas_per_sm();  // resident CTAs per SM the launch grid is sized for
 cudaError_t launch_sparse_attn(const AttnLaunch &a, int d, int bs, cudaStream_t stream);
-// Cached keys: bs = 128; n_items = B * heads * row_tiles, `order` and the CSR unused.
+// Cached keys: bs = 128; n_items = the whole items from the queue (CacheTiles::n_whole), `order` and the CSR
+// unused.
 cudaError_t launch_cache_tiles(const AttnLaunch &a, const CacheTiles &ct, int d, cudaStream_t stream);
 // e4m3 operands (tmap_* over uint8 codes), d = 128, bs in {64, 128}.
 cudaError_t launch_sparse_attn_fp8(const AttnLaunch &a, int bs, cudaStream_t stream);

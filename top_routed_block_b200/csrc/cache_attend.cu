@@ -49,8 +49,8 @@
 // atomics, the same bits every time.  Caches of at most 512 tokens take one CTA a segment and row
 // tile, and one launch.
 //
-// Measured: one token of 8 sequences x 40 heads, 88 k tokens, d 128 (902 MB) 141.5 us, 6.4 TB/s, and 4.4 us
-// for the join.  Row tiles beyond the first are bound by the conversion of V (the ALU pipe is busy 48 % of
+// Measured: one token of 8 sequences x 40 heads, 88 k tokens, d 128 (902 MB) 144.5 us with the join (4.4 alone),
+// 6.2 TB/s.  Row tiles beyond the first are bound by the conversion of V (the ALU pipe is busy 48 % of
 // the time, 12 warps an SM hide no more): 20 rows of 4 x 8 heads, 20 k tokens (41 MB) 27 + 4 us.  Short
 // segments cost their beginning and end: 256 sequences of 200 to 2000 tokens x 8 heads (590 MB) 143 us.
 #include <cuda_bf16.h>
@@ -75,7 +75,16 @@ constexpr int kRows = 8;                // rows of a tile
 // heads, 88 k tokens, d 128: 141 us, with 64 149).  More tiles, bound by the warps: 64, which
 // spends less on each token (20 rows, 4 x 8 heads, 20 k tokens: 27 us, with 32 34).
 constexpr int kOneTileStep = 32, kMoreTilesStep = 64;
-constexpr int kWholeTokens = 512;       // caches this short: a CTA takes a whole segment
+// Tables of at most so many tokens: a CTA takes a whole segment, in one launch without a plan.  us, whole / split, in
+// tables of just the cached tokens, one row (20 rows):
+//   cached tokens           250                    500                     1000                    2000
+//   8 heads, d 64            5.2 /  9.5 (5.4, 9.9)   6.1 /  9.8 (6.4, 10.7)   8.2 /  9.7 (8.4, 10.7)  12.0 /  9.9 (12.4, 11.0)
+//   8 heads, d 128           6.3 / 10.4 (7.4, 12.2)  7.6 / 10.7 (8.7, 12.7)  10.2 / 11.1 (11.4, 13.0) 15.5 / 11.4 (16.9, 14.0)
+//   8 sequences x 40, d 128  8.9 / 13.8             12.6 / 17.4             19.7 / 24.5             35.6 / 38.5
+// They meet between 1000 and 1500 tokens, later with more segments; 512 lies on the safe side.  The rule
+// sees the table's width, not the lengths, which are on the device: the same 500 tokens of 8 heads, d 128, take 7.6 us
+// in a table of 512 and 10.9 in one of 65536.
+constexpr int kWholeTokens = 512;
 constexpr int kCtasPerSm = 3;           // by shared memory (64 KB each at d 128) and registers
 constexpr int kChunkShare = 8;          // units per CTA below which segments are cut into chunks
 constexpr int kChunkSequences = 64;     // more sequences are not worth the search for the chunk
@@ -905,7 +914,8 @@ int few_ctas(int sms) { return sms * kCtasPerSm - 1; }
 // and is the same from 1 to 128 rows.  They meet at about 64 (us, few / tiles: d 128, 4 x 8 heads, 93 k
 // tokens in all: 48 rows 148 / 183, 64 rows 189 / 184, 96 rows 283 / 185; 23 k tokens: 54 / 64, 67 / 63,
 // 94 / 64; d 64, 23 k: 36 / 49, 44 / 48, 61 / 49), and at 128 where a CTA takes a whole cache and nothing
-// is joined (500 tokens: 96 rows 15 / 23, 128 rows 20 / 23).
+// is joined (500 tokens: 96 rows 15 / 23, 128 rows 20 / 23; that is for few segments: 100 rows of 8 heads, d 128, with 8
+// sequences 27 / 35, with 32 97 / 64).
 bool attend_few_rows(int group, int M, int64_t capacity) {
     return attend_rows(group, M) <= (capacity <= kWholeTokens ? 128 : 64);
 }

@@ -162,9 +162,14 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const int32_t 
     const int64_t tiles = ceil_div(N, tokens);
     const int heads = q.heads + k.heads;
     // Two token tiles per SM or more: one group of all heads, so that a token's angles are computed
-    // once.  Fewer: the heads are split until there are about three CTAs per SM.  Measured, us
-    // (40 heads x 32760 tokens d 128; 8 x 32768 d 64; 3 x 7 heads x 1571 d 128): long form 209.3,
-    // 24.9, 11.2; short form 213.7, 26.9, 8.7.
+    // once.  Fewer: the heads are split until there are about three CTAs per SM.  Measured on both sides
+    // of the switch, Q and K of so many heads each, d 128, us, short form / long form:
+    //   token tiles per SM    0.25         0.5          1            2            3            8
+    //   40 heads              10.9 / 21.3  18.8 / 23.4  34.8 / 32.8  69.2 / 68.4  103 / 95.5   254 / 240
+    //    8 heads               3.5 / 5.4    6.1 / 6.7    9.2 / 9.1   15.7 / 15.1  21.8 / 21.3  53.2 / 50.1
+    //    2 heads               2.4 / 3.4    3.0 / 3.5    3.4 / 4.0    6.0 / 6.2    7.3 / 10.6  15.8 / 22.0
+    // (d 64 alike.)  They meet between one and two tiles per SM.  With fewer heads than the long form
+    // has in flight (2 + 2 of 8) it stays behind throughout; the rule does not look at that.
     const bool is_long = tiles * B >= 2LL * sms;
     const int64_t groups_wanted = is_long ? 1 : ceil_div(3LL * sms, tiles * B);
     const int per_group = static_cast<int>(ceil_div(heads, groups_wanted < heads ? groups_wanted : heads));
